@@ -60,6 +60,7 @@ extern "C" {
 #define DSA_ROPE 64         /* qk_rope_head_dim */
 #define DSA_ROW 576         /* DSA_LATENT + DSA_ROPE: one latent-cache row / one latent query */
 #define DSA_MAX_TOPK 2048   /* index_topk */
+#define DSA_ROW8 640        /* bytes of one row of the paged 8-bit cache: 512 codes, 64 bf16 */
 
 typedef uint16_t dsa_bf16;             /* bf16 bit pattern */
 typedef struct CUstream_st* dsa_stream_t; /* same type as cudaStream_t */
@@ -81,7 +82,8 @@ enum dsa_op {
   DSA_OP_FORWARD = 3,
   DSA_OP_INDEXER_TOPK = 4,
   DSA_OP_DENSE_SPARSE = 5,
-  DSA_OP_BLOCK_SPARSE = 6
+  DSA_OP_BLOCK_SPARSE = 6,
+  DSA_OP_PAGED_MLA = 7
 };
 
 /*
@@ -273,6 +275,102 @@ DSA_API int dsa_forward(const dsa_bf16* q_I, const dsa_bf16* w, const dsa_bf16* 
 DSA_API int dsa_indexer_scores_noalloc(const dsa_bf16* q_I, const dsa_bf16* w, const dsa_bf16* k_I,
                                        int64_t cache_rows, const int64_t* kv_start, const int32_t* n_vis, int T,
                                        float* scores, int64_t score_ld, dsa_stream_t stream);
+
+/*
+ * The paged 8-bit latent cache.  The pages keep every position in the cache
+ * and say nothing of how it is stored ("From a trillion dot products to two
+ * thousand: how DSA breaks N^2", section on skipped tokens); the four entry
+ * points below are a storage form of this library and the attention over it.
+ *
+ * Cache row (644 bytes instead of 1152).  For a latent row (c_kv || k_rope) let
+ * k be the smallest whole number with max |c_kv| <= 448 * 2^k over its finite
+ * values, held to [-60, 60] (-60 when all are zero).  Then
+ *     kv8[row, 0:512]   = c_kv * 2^-k rounded to e4m3 (nearest, ties to even;
+ *                         beyond +-448 the largest code; NaN and infinities: NaN)
+ *     kv8[row, 512:640] = k_rope * 2^-k as 64 bf16
+ *     kv_scale[row]     = 2^k
+ * Only the e4m3 code is a rounding: the rope half is exact for magnitudes in
+ * [2^-66, 2^67], and a code times 2^k is exact in bf16.
+ *
+ * Batch.  `batch` sequences; sequence b's cache is pages page_table[b, 0 ..],
+ * position s in row page_table[b, s / page_size] * page_size + s % page_size.
+ * Its new tokens are the query rows cu_q[b] .. cu_q[b+1]-1 (any number, also
+ * none) and the last of its seq_len[b] positions: row t stands at position
+ * seq_len[b] - (cu_q[b+1] - t) and sees the positions up to its own.  Query
+ * rows from cu_q[batch] on belong to no sequence and are left alone.
+ *
+ *  T           rows of the row tensors, at least cu_q[batch]
+ *  cu_q        [batch+1] int32 (device), not decreasing
+ *  seq_len     [batch] int32 (device), 0 .. max_pages * page_size
+ *  page_table  [batch,max_pages] int32 (device); only the entries of pages that
+ *              hold a visible position are read
+ *  kv8         [n_pages,page_size,640] bytes, 16-byte aligned; kv_scale [n_pages,page_size] fp32;
+ *              any page_size >= 1, n_pages * page_size <= 2^31-1
+ * A query row whose numbers do not fit together, or a page outside the cache,
+ * sets the status bit (dsa_sync_status: DSA_ERR_BAD_ROW); what each entry point
+ * then does with the row stands below.
+ */
+
+/*
+ * Quantise the latent rows of the new tokens and write them to their places in
+ * the cache.  Rows without a place (see above) are not written; nothing else in
+ * the cache changes.  No two rows of a call may have the same place (page
+ * tables that share a page that is written): its content is then undefined.
+ *
+ *  rows  [T] rows of c_kv || k_rope (576 bf16), rows_ld elements apart
+ *        (rows_ld >= 576, a multiple of 8), 16-byte aligned
+ */
+DSA_API int dsa_cache_write(const dsa_bf16* rows, int64_t rows_ld, int T, const int32_t* cu_q, const int32_t* seq_len,
+                            const int32_t* page_table, int batch, int max_pages, uint8_t* kv8, float* kv_scale,
+                            int n_pages, int page_size, dsa_stream_t stream);
+
+/*
+ * Read the cache back: for every sequence b and s < seq_len[b], the flat row
+ *     kv[kv_start[b] + s, :] = 2^k (codes || rope)   in bf16,
+ * the layout that dsa_forward, dsa_sparse_mla_attn and the others read.  Other
+ * rows of kv are left as they were; so are those of a sequence whose seq_len or
+ * kv_start does not fit (status bit), and those in a page outside the cache.
+ *
+ *  kv_start [batch] int64 (device); kv [cache_rows,576] bf16, 16-byte aligned
+ */
+DSA_API int dsa_cache_read(const uint8_t* kv8, const float* kv_scale, int n_pages, int page_size,
+                           const int32_t* seq_len, const int32_t* page_table, int batch, int max_pages,
+                           const int64_t* kv_start, dsa_bf16* kv, int64_t cache_rows, dsa_stream_t stream);
+
+/*
+ * Dense latent attention of the new tokens over their sequences' pages: the
+ * attention of dsa_sparse_mla_attn (same formulas, same scale) over every
+ * position that a query row sees.  One token a sequence is a decode step,
+ * several check drafted tokens, many are a prompt's chunk; the cache must
+ * already hold the new tokens' own rows (dsa_cache_write before it on the stream).
+ *
+ *  q      [T,64,576] bf16, 16-byte aligned
+ *  o_lat  [T,64,512] bf16, 16-byte aligned (bf16 here: what follows is a product
+ *         with bf16 weights); lse [T,64] fp32 or NULL
+ *  ws     >= dsa_workspace_size(DSA_OP_PAGED_MLA, T, max_pages * page_size, 0) bytes,
+ *         256-byte aligned: partial results of rows that are split over CTAs
+ * A row that sees nothing, or whose numbers do not fit (status bit), gets
+ * o_lat = 0 and lse = -inf; a position in a page outside the cache is skipped
+ * (status bit).
+ */
+DSA_API int dsa_paged_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len,
+                               const int32_t* page_table, int batch, int max_pages, const uint8_t* kv8,
+                               const float* kv_scale, int n_pages, int page_size, float scale, dsa_bf16* o_lat,
+                               float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * The same over each row's selected positions, as dsa_topk and dsa_indexer_topk
+ * write them: dsa_sparse_mla_attn over the paged 8-bit cache.
+ *
+ *  idx  [T,topk] int32, 1 <= topk <= 2048: positions in the row's sequence, -1 =
+ *       empty slot; an entry at or beyond what the row sees is skipped (status bit)
+ *  ws   >= dsa_workspace_size(DSA_OP_PAGED_MLA, T, max_pages * page_size, topk) bytes, 256-byte aligned
+ */
+DSA_API int dsa_paged_sparse_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len,
+                                      const int32_t* page_table, int batch, int max_pages, const int32_t* idx,
+                                      int topk, const uint8_t* kv8, const float* kv_scale, int n_pages, int page_size,
+                                      float scale, dsa_bf16* o_lat, float* lse, void* ws, size_t ws_bytes,
+                                      dsa_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the device status word of the

@@ -16,10 +16,11 @@ LIB_PATH = os.path.join(PKG, "libdsa.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_UNSUPPORTED, DSA_ERR_BAD_ROW = range(7)
 (DSA_OP_INDEXER, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_FORWARD, DSA_OP_INDEXER_TOPK, DSA_OP_DENSE_SPARSE,
- DSA_OP_BLOCK_SPARSE) = range(7)
+ DSA_OP_BLOCK_SPARSE, DSA_OP_PAGED_MLA) = range(8)
 BLOCK_TOPK = 16
 INDEX_HEADS, INDEX_DIM, HEADS, LATENT, ROPE, ROW, MAX_TOPK = 32, 128, 64, 512, 64, 576, 2048
 NOALLOC_MAX_ROWS = 8192
+ROW8 = 640
 
 _STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_WORKSPACE", 3: "DSA_ERR_CUDA",
                  4: "DSA_ERR_TIMEOUT", 5: "DSA_ERR_UNSUPPORTED", 6: "DSA_ERR_BAD_ROW"}
@@ -57,6 +58,14 @@ def lib():
         L.dsa_indexer_scores_noalloc.restype = I
         L.dsa_block_sparse_attn.argtypes = [P, P, P, P, P, I64, P, P, I, I64, P, F, P, P, P, P, SZ, P]
         L.dsa_block_sparse_attn.restype = I
+        paged = [P, P, P, I, I]             # cu_q, seq_len, page_table, batch, max_pages
+        cache = [P, P, I, I]                # kv8, kv_scale, n_pages, page_size
+        L.dsa_cache_write.argtypes = [P, I64, I, *paged, *cache, P]
+        L.dsa_cache_read.argtypes = [*cache, P, P, I, I, P, P, I64, P]
+        L.dsa_paged_mla_attn.argtypes = [P, I, *paged, *cache, F, P, P, P, SZ, P]
+        L.dsa_paged_sparse_mla_attn.argtypes = [P, I, *paged, P, I, *cache, F, P, P, P, SZ, P]
+        for name in ("dsa_cache_write", "dsa_cache_read", "dsa_paged_mla_attn", "dsa_paged_sparse_mla_attn"):
+            getattr(L, name).restype = I
         L.dsa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
         L.dsa_set_wait_limit_ns.restype = None
         L.dsa_check_wait_timeout.argtypes = [P]
@@ -243,6 +252,97 @@ def dsa_block_sparse_attn(q_I, w, k_I, q, kv, kv_start, n_vis, max_n_vis, gates,
     _check(lib().dsa_block_sparse_attn(_ptr(q_I), _ptr(w), _ptr(k_I), _ptr(q), _ptr(kv), kv.shape[0], _ptr(kv_start),
                                        _ptr(n_vis), T, int(max_n_vis), _ptr(gates), float(scale), _ptr(o_lat),
                                        _ptr(lse), _ptr(blocks_out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _need_paged(seq_len, page_table, kv8, kv_scale, cu_q=None):
+    """Check the batch's description and the cache; (batch, max_pages, n_pages, page_size)."""
+    import torch
+    _need(seq_len, torch.int32, None, "seq_len")
+    batch = seq_len.numel()
+    _need(seq_len, torch.int32, (batch,), "seq_len")
+    if cu_q is not None:
+        _need(cu_q, torch.int32, (batch + 1,), "cu_q")
+    _need(kv8, torch.uint8, None, "kv8")
+    if kv8.dim() != 3 or kv8.shape[2] != ROW8:
+        raise ValueError(f"kv8 must have shape (n_pages, page_size, {ROW8}), got {tuple(kv8.shape)}")
+    _need(kv_scale, torch.float32, kv8.shape[:2], "kv_scale")
+    _need(page_table, torch.int32, None, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"page_table must have shape ({batch}, max_pages), got {tuple(page_table.shape)}")
+    return batch, page_table.shape[1], kv8.shape[0], kv8.shape[1]
+
+
+def _on_current_device(*tensors):
+    """The kernels run on the current device: a tensor of another one would be a wild pointer to them."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
+
+
+def dsa_cache_write(rows, cu_q, seq_len, page_table, kv8, kv_scale, stream=None):
+    """Quantise latent rows [T, 576] bf16 (their row stride is free, the rest contiguous)
+    into the paged cache kv8 [n_pages, page_size, 640] uint8, kv_scale [n_pages, page_size]."""
+    import torch
+    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
+    if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype != torch.bfloat16:
+        raise TypeError("rows must be a CUDA tensor of torch.bfloat16")
+    if rows.dim() != 2 or rows.shape[1] != ROW or rows.stride(1) != 1:
+        raise ValueError(f"rows must have shape (T, {ROW}) with contiguous rows, got {tuple(rows.shape)}, "
+                         f"strides {rows.stride()}")
+    _on_current_device(rows, cu_q, seq_len, page_table, kv8, kv_scale)
+    T = rows.shape[0]
+    ld = rows.stride(0) if T > 1 else ROW
+    _check(lib().dsa_cache_write(_ptr(rows), ld, T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
+                                 _ptr(kv8), _ptr(kv_scale), n_pages, page_size, _stream(stream)))
+
+
+def dsa_cache_read(kv8, kv_scale, seq_len, page_table, kv_start, kv, stream=None):
+    """Unpack every sequence of the paged cache to flat bf16 rows kv[kv_start[b] + s]."""
+    import torch
+    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale)
+    _need(kv_start, torch.int64, (batch,), "kv_start")
+    _need(kv, torch.bfloat16, (kv.shape[0], ROW), "kv")
+    _on_current_device(kv8, kv_scale, seq_len, page_table, kv_start, kv)
+    _check(lib().dsa_cache_read(_ptr(kv8), _ptr(kv_scale), n_pages, page_size, _ptr(seq_len), _ptr(page_table), batch,
+                                max_pages, _ptr(kv_start), _ptr(kv), kv.shape[0], _stream(stream)))
+
+
+def _need_paged_attn(q, o_lat, lse, ws):
+    import torch
+    T = q.shape[0]
+    _need(q, torch.bfloat16, (T, HEADS, ROW), "q")
+    _need(o_lat, torch.bfloat16, (T, HEADS, LATENT), "o_lat")
+    if lse is not None:
+        _need(lse, torch.float32, (T, HEADS), "lse")
+    _need(ws, torch.uint8, None, "ws")
+    return T
+
+
+def dsa_paged_mla_attn(q, cu_q, seq_len, page_table, kv8, kv_scale, scale, o_lat, lse, ws, stream=None):
+    """Dense latent attention of the new tokens over their sequences' pages; o_lat is bf16, lse may be None."""
+    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
+    T = _need_paged_attn(q, o_lat, lse, ws)
+    _on_current_device(q, cu_q, seq_len, page_table, kv8, kv_scale, o_lat, lse, ws)
+    _check(lib().dsa_paged_mla_attn(_ptr(q), T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
+                                    _ptr(kv8), _ptr(kv_scale), n_pages, page_size, float(scale), _ptr(o_lat),
+                                    _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def dsa_paged_sparse_mla_attn(q, cu_q, seq_len, page_table, idx, kv8, kv_scale, scale, o_lat, lse, ws, stream=None):
+    """Latent attention of the new tokens over their selected positions idx [T, topk] of the paged cache."""
+    import torch
+    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
+    T = _need_paged_attn(q, o_lat, lse, ws)
+    _need(idx, torch.int32, None, "idx")
+    if idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError(f"idx must have shape ({T}, topk), got {tuple(idx.shape)}")
+    _on_current_device(q, cu_q, seq_len, page_table, idx, kv8, kv_scale, o_lat, lse, ws)
+    _check(lib().dsa_paged_sparse_mla_attn(_ptr(q), T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
+                                           _ptr(idx), idx.shape[1], _ptr(kv8), _ptr(kv_scale), n_pages, page_size,
+                                           float(scale), _ptr(o_lat), _ptr(lse), _ptr(ws), ws.numel(),
+                                           _stream(stream)))
 
 
 def dsa_sync_status(stream=None):

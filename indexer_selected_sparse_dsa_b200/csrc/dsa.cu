@@ -20,6 +20,8 @@
 #include "block_sparse.cuh"
 #include "dense_sparse.cuh"
 #include "indexer.cuh"
+#include "paged_cache.cuh"
+#include "paged_mla.cuh"
 #include "sparse_mla.cuh"
 #include "topk.cuh"
 #include "decode_fused.cuh"
@@ -307,6 +309,63 @@ int check_common_rows(int T, int64_t cache_rows, const void* kv_start) {
   return DSA_OK;
 }
 
+// The page table, the cache and the batch's description, as every paged entry point takes them.
+int check_paged(const int32_t* cu_q, const int32_t* seq_len, const int32_t* page_table, int batch, int max_pages,
+                const void* kv8, const float* kv_scale, int n_pages, int page_size) {
+  if (batch < 0) return fail(DSA_ERR_INVALID_ARG, "batch must be >= 0 (got %d)", batch);
+  if (max_pages < 1 || n_pages < 1 || page_size < 1)
+    return fail(DSA_ERR_INVALID_ARG, "max_pages, n_pages and page_size must be >= 1 (got %d, %d, %d)", max_pages,
+                n_pages, page_size);
+  if (int64_t(n_pages) * page_size > INT32_MAX)
+    return fail(DSA_ERR_INVALID_ARG, "n_pages * page_size must be at most 2^31-1");
+  if (batch == 0) return DSA_OK;
+  if (!cu_q || !seq_len || !page_table || !kv8 || !kv_scale)
+    return fail(DSA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(kv8, 16)) return fail(DSA_ERR_INVALID_ARG, "kv8 must be 16-byte aligned");
+  if (!aligned(cu_q, 4) || !aligned(seq_len, 4) || !aligned(page_table, 4) || !aligned(kv_scale, 4))
+    return fail(DSA_ERR_INVALID_ARG, "cu_q, seq_len, page_table, kv_scale must be 4-byte aligned");
+  return DSA_OK;
+}
+
+size_t ws_paged_mla(int T, int64_t max_n_vis) { return 0; }
+
+// idx == nullptr: every visible position
+int run_paged_mla(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len, const int32_t* page_table,
+                  int batch, int max_pages, const int32_t* idx, int topk, const uint8_t* kv8, const float* kv_scale,
+                  int n_pages, int page_size, float scale, dsa_bf16* o_lat, float* lse, void* ws, size_t ws_bytes,
+                  dsa_stream_t stream) {
+  t_err.clear();
+  if (T < 0) return fail(DSA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+  int rc = check_paged(cu_q, seq_len, page_table, batch, max_pages, kv8, kv_scale, n_pages, page_size);
+  if (rc) return rc;
+  if (T == 0 || batch == 0) return DSA_OK;
+  if (!q || !o_lat) return fail(DSA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(q, 16) || !aligned(o_lat, 16) || !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "q, o_lat must be 16-byte aligned and lse 4-byte aligned");
+  if (!(scale > 0.f) || !(scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (int64_t(T) * DSA_HEADS > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "T too large");
+  DeviceState* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  dsa::PagedMlaLaunch p{};
+  p.q = q;
+  p.T = T;
+  p.cu_q = cu_q;
+  p.seq_len = seq_len;
+  p.idx = idx;
+  p.topk = topk;
+  p.cache = {const_cast<uint8_t*>(kv8), const_cast<float*>(kv_scale), page_table, batch, max_pages, n_pages, page_size};
+  p.scale = scale;
+  p.o_lat = o_lat;
+  p.lse = lse;
+  p.part = static_cast<float*>(ws);
+  p.sm_count = dev->sm_count;
+  p.wait_ns = wait_limit_ns();
+  p.stream = stream;
+  cudaError_t e = dsa::launch_paged_mla(p);
+  if (e != cudaSuccess) return cuda_fail(e, "paged MLA launch");
+  return DSA_OK;
+}
+
 int run_sparse_mla(const dsa::MlaLaunch& p) {
   if (int64_t(p.T) * DSA_HEADS > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "T too large");
   CUtensorMap tq;
@@ -390,6 +449,7 @@ size_t dsa_workspace_size(int op, int T, int64_t max_n_vis, int topk) {
     case DSA_OP_FORWARD: return ws_forward(T, max_n_vis, topk);
     case DSA_OP_INDEXER_TOPK: return ws_indexer(T) + ws_select(T);
     case DSA_OP_DENSE_SPARSE: return ws_dense_sparse(T);
+    case DSA_OP_PAGED_MLA: return ws_paged_mla(T, topk > 0 ? topk : max_n_vis);
     case DSA_OP_BLOCK_SPARSE: return max_n_vis > 0 ? block_layout(T, max_n_vis).total : 0;
     default: return 0;
   }
@@ -723,6 +783,66 @@ int dsa_check_wait_timeout(dsa_stream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "wait probe launch");
   return DSA_OK;
+}
+
+int dsa_cache_write(const dsa_bf16* rows, int64_t rows_ld, int T, const int32_t* cu_q, const int32_t* seq_len,
+                    const int32_t* page_table, int batch, int max_pages, uint8_t* kv8, float* kv_scale, int n_pages,
+                    int page_size, dsa_stream_t stream) {
+  t_err.clear();
+  if (T < 0) return fail(DSA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+  int rc = check_paged(cu_q, seq_len, page_table, batch, max_pages, kv8, kv_scale, n_pages, page_size);
+  if (rc) return rc;
+  if (T == 0 || batch == 0) return DSA_OK;
+  if (!rows) return fail(DSA_ERR_INVALID_ARG, "rows is NULL");
+  if (!aligned(rows, 16)) return fail(DSA_ERR_INVALID_ARG, "rows must be 16-byte aligned");
+  if (rows_ld < DSA_ROW || rows_ld % 8 != 0)
+    return fail(DSA_ERR_INVALID_ARG, "rows_ld must be a multiple of 8, at least %d (got %lld)", DSA_ROW, (long long)rows_ld);
+  DeviceState* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  dsa::CacheWriteLaunch p{rows, rows_ld, T, cu_q, seq_len,
+                          {kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size}, stream};
+  cudaError_t e = dsa::launch_cache_write(p);
+  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+  return DSA_OK;
+}
+
+int dsa_cache_read(const uint8_t* kv8, const float* kv_scale, int n_pages, int page_size, const int32_t* seq_len,
+                   const int32_t* page_table, int batch, int max_pages, const int64_t* kv_start, dsa_bf16* kv,
+                   int64_t cache_rows, dsa_stream_t stream) {
+  t_err.clear();
+  int rc = check_paged(seq_len, seq_len, page_table, batch, max_pages, kv8, kv_scale, n_pages, page_size);
+  if (rc) return rc;
+  if (batch == 0) return DSA_OK;
+  if ((rc = check_common_rows(batch, cache_rows, kv_start))) return rc;
+  if (!kv) return fail(DSA_ERR_INVALID_ARG, "kv is NULL");
+  if (!aligned(kv, 16)) return fail(DSA_ERR_INVALID_ARG, "kv must be 16-byte aligned");
+  DeviceState* dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  dsa::CacheReadLaunch p{{const_cast<uint8_t*>(kv8), const_cast<float*>(kv_scale), page_table, batch, max_pages, n_pages,
+                          page_size}, seq_len, kv_start, kv, cache_rows, dev->sm_count, stream};
+  cudaError_t e = dsa::launch_cache_read(p);
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return DSA_OK;
+}
+
+int dsa_paged_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len,
+                       const int32_t* page_table, int batch, int max_pages, const uint8_t* kv8, const float* kv_scale,
+                       int n_pages, int page_size, float scale, dsa_bf16* o_lat, float* lse, void* ws, size_t ws_bytes,
+                       dsa_stream_t stream) {
+  return run_paged_mla(q, T, cu_q, seq_len, page_table, batch, max_pages, nullptr, 0, kv8, kv_scale, n_pages,
+                       page_size, scale, o_lat, lse, ws, ws_bytes, stream);
+}
+
+int dsa_paged_sparse_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len,
+                              const int32_t* page_table, int batch, int max_pages, const int32_t* idx, int topk,
+                              const uint8_t* kv8, const float* kv_scale, int n_pages, int page_size, float scale,
+                              dsa_bf16* o_lat, float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  t_err.clear();
+  if (topk < 1 || topk > DSA_MAX_TOPK) return fail(DSA_ERR_INVALID_ARG, "topk must lie in [1, %d]", DSA_MAX_TOPK);
+  if (T > 0 && batch > 0 && (!idx || !aligned(idx, 4)))
+    return fail(DSA_ERR_INVALID_ARG, "idx must not be NULL and must be 4-byte aligned");
+  return run_paged_mla(q, T, cu_q, seq_len, page_table, batch, max_pages, idx, topk, kv8, kv_scale, n_pages, page_size,
+                       scale, o_lat, lse, ws, ws_bytes, stream);
 }
 
 int dsa_sync_status(dsa_stream_t stream) {

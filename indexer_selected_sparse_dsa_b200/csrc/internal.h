@@ -122,6 +122,55 @@ cudaError_t launch_block_expand(const int32_t* blocks, const int32_t* n_vis, int
 cudaError_t launch_fuse3(float* o, const float* o_loc, const float* o_anc, const float* gates, int T, int sm_count,
                          cudaStream_t stream);
 
+// ------------------------------------------------------------------ paged 8-bit latent cache
+// Sequence b's position s lies in page page_table[b, s / page_size].
+struct PagedCache {
+  uint8_t* kv8;               // [n_pages * page_size, 640]: 512 e4m3 codes, 64 bf16
+  float* kv_scale;            // [n_pages * page_size]: the row's power of two
+  const int32_t* page_table;  // [batch, max_pages]
+  int batch;
+  int max_pages;
+  int n_pages;
+  int page_size;
+};
+struct CacheWriteLaunch {
+  const uint16_t* rows;
+  int64_t rows_ld;
+  int T;
+  const int32_t* cu_q;
+  const int32_t* seq_len;
+  PagedCache cache;
+  cudaStream_t stream;
+};
+cudaError_t launch_cache_write(const CacheWriteLaunch& p);
+struct CacheReadLaunch {
+  PagedCache cache;
+  const int32_t* seq_len;
+  const int64_t* kv_start;
+  uint16_t* kv;
+  int64_t cache_rows;
+  int sm_count;
+  cudaStream_t stream;
+};
+cudaError_t launch_cache_read(const CacheReadLaunch& p);
+struct PagedMlaLaunch {
+  const uint16_t* q;
+  int T;
+  const int32_t* cu_q;
+  const int32_t* seq_len;
+  const int32_t* idx;  // selected positions [T, topk], or null: every visible position
+  int topk;
+  PagedCache cache;
+  float scale;
+  uint16_t* o_lat;
+  float* lse;
+  float* part;  // split partials
+  int sm_count;
+  unsigned long long wait_ns;
+  cudaStream_t stream;
+};
+cudaError_t launch_paged_mla(const PagedMlaLaunch& p);
+
 // ------------------------------------------------------------------ fused decode step
 // The whole step of a batch of at most kDecodeMaxRows query rows in one
 // cooperative launch (one CTA per SM): indexer, exact top-k, attention, merge.
