@@ -94,6 +94,7 @@ int current_device(DeviceState** out) {
   if (!d.prepared) {
     if ((e = dsa::prepare_indexer()) != cudaSuccess) return cuda_fail(e, "indexer smem opt-in");
     if ((e = dsa::prepare_sparse_mla()) != cudaSuccess) return cuda_fail(e, "sparse MLA smem opt-in");
+    if ((e = dsa::prepare_paged_mla()) != cudaSuccess) return cuda_fail(e, "paged MLA smem opt-in");
     if ((e = dsa::prepare_topk()) != cudaSuccess) return cuda_fail(e, "top-k smem opt-in");
     if ((e = dsa::prepare_decode_fused()) != cudaSuccess) return cuda_fail(e, "fused decode smem opt-in");
     d.prepared = true;
@@ -327,7 +328,10 @@ int check_paged(const int32_t* cu_q, const int32_t* seq_len, const int32_t* page
   return DSA_OK;
 }
 
-size_t ws_paged_mla(int T, int64_t max_n_vis) { return 0; }
+// max_keys: the keys a query row can have (its selection, or the longest sequence)
+size_t ws_paged_mla(int T, int64_t max_keys) {
+  return T > 0 && max_keys > 0 ? align_up(dsa::paged_mla_ws_bytes(T, max_keys), 256) : 0;
+}
 
 // idx == nullptr: every visible position
 int run_paged_mla(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len, const int32_t* page_table,
@@ -344,6 +348,9 @@ int run_paged_mla(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* 
     return fail(DSA_ERR_INVALID_ARG, "q, o_lat must be 16-byte aligned and lse 4-byte aligned");
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
   if (int64_t(T) * DSA_HEADS > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "T too large");
+  if (!ws || !aligned(ws, 256)) return fail(DSA_ERR_INVALID_ARG, "ws must not be NULL and must be 256-byte aligned");
+  const size_t need = ws_paged_mla(T, idx ? topk : int64_t(max_pages) * page_size);
+  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "workspace %zu < required %zu bytes", ws_bytes, need);
   DeviceState* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   dsa::PagedMlaLaunch p{};
@@ -357,7 +364,7 @@ int run_paged_mla(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* 
   p.scale = scale;
   p.o_lat = o_lat;
   p.lse = lse;
-  p.part = static_cast<float*>(ws);
+  p.ws = ws;
   p.sm_count = dev->sm_count;
   p.wait_ns = wait_limit_ns();
   p.stream = stream;

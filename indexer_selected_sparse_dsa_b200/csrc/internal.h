@@ -164,7 +164,7 @@ struct PagedMlaLaunch {
   float scale;
   uint16_t* o_lat;
   float* lse;
-  float* part;  // split partials
+  void* ws;            // split rows' partial results
   int sm_count;
   unsigned long long wait_ns;
   cudaStream_t stream;
@@ -205,6 +205,7 @@ cudaError_t launch_decode_fused(const DecodeFusedLaunch& p, const CUtensorMap& t
 cudaError_t prepare_indexer();
 cudaError_t prepare_sparse_mla();
 cudaError_t prepare_topk();
+cudaError_t prepare_paged_mla();
 cudaError_t prepare_decode_fused();
 // Exact top-k of each query's candidate buffer (after the streamed sweep),
 // written ascending and -1 padded; rows with cnt_out < 0 are left as they are.

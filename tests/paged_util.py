@@ -80,6 +80,10 @@ class Batch:
         x = torch.cat([tab[raw[:, :LATENT].long()], raw[:, LATENT:].contiguous().view(torch.bfloat16).double()], 1)
         return x * self.kv_scale.view(-1)[at].double()[:, None]
 
+    def scales(self, b, n):
+        import torch
+        return self.kv_scale.view(-1)[torch.from_numpy(self.slots(b, np.arange(n))).cuda()].double()
+
     def outputs(self):
         import torch
         o = torch.full((self.T, HEADS, LATENT), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -93,6 +97,9 @@ class Batch:
         off by at most e = scale * (2^-17 sum |q||k| + 2^-22 max|q| sum |k|) plus 2^-20 for the exponential's argument
         and itself.  Probabilities are rounded to fp16, 2^-11, and sums in 32 bits again, 2^-17; the output to bf16,
         2^-8 of itself.  A relative error e of every weight moves a mean by at most 2 e times the mean magnitude.
+        fp16 has a floor besides its relative step: what is rounded is u = p 2^k, held so that the largest u of a head
+        is at least 2^6 (the running maximum stands at 2^6 and is never above a score already seen); values below 2^-14
+        are rounded to multiples of 2^-24, so each u is off by up to 2^-25 more, 2^-31 of the largest, times its code.
         """
         import torch
         o = torch.zeros(self.T, HEADS, LATENT, dtype=torch.float64, device="cuda")
@@ -101,14 +108,15 @@ class Batch:
         for b, (n, m) in enumerate(zip(self.new, self.lens)):
             if n == 0 or m == 0:
                 continue
-            seq = self.values(b, m)
+            seq, sc = self.values(b, m), self.scales(b, m)
             for j in range(n):
                 t = int(self.cu[b]) + j
                 seen = m - n + j + 1
-                k = seq[:seen]
+                k, ks = seq[:seen], sc[:seen]
                 if idx is not None:
                     s = torch.as_tensor(idx[t]).long().cuda()
-                    k = seq[s[(s >= 0) & (s < seen)]]
+                    s = s[(s >= 0) & (s < seen)]
+                    k, ks = seq[s], sc[s]
                 if k.shape[0] == 0:
                     continue
                 q = self.q[t].double()
@@ -121,6 +129,7 @@ class Batch:
                              + 2.0 ** -22 * q.abs().amax(1, keepdim=True) * k.abs().sum(1)[None]).amax(1) + 2.0 ** -20
                 tl[t] = e + 2.0 ** -22 * lse[t].abs()
                 to[t] = 2.0 ** -8 * o[t].abs() + (2 * e[:, None] + 2.0 ** -11 + 2.0 ** -16) * (p @ v.abs())
+                to[t] += 2.0 ** -31 * (p * ks).amax(1)[:, None] * (v.abs() / ks[:, None]).sum(0)[None]
         return o, lse, to, tl
 
 
