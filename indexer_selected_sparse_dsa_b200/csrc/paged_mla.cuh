@@ -15,20 +15,20 @@
 // Values as fp16.  A code is exact in fp16, and a probability rounded to fp16
 // (2^-11) is eight times closer than one in bf16.  The row's 2^k goes into the
 // probability: with y = S log2(e) + k_s, u_s = 2^(y - m + 6) where m follows
-// the running maximum of y, so u is at most 2^14 (see kLazyRescale) and what
+// the running maximum of y in whole numbers, so u is at most 2^14 (see kLazyRescale) and what
 // fp16 cannot hold is 2^-31 of the largest; sum u code is the numerator,
 // sum u 2^-k_s (fp32, u before rounding) the denominator.
 //
 // One CTA walks an equal share of all 128-key tiles of the batch, query row
 // after query row; a row that ends in another CTA leaves partial sums that
-// paged_mla_merge_kernel joins.  20 warps (five per scheduler: 96 registers a thread):
+// paged_mla_merge_kernel joins.  16 warps:
 //  * warp 3 finds each key's cache row and 2^k, up to four tiles ahead;
 //  * warps 0 and 1 copy the tile's rows (four chunks of 128 codes, then
 //    the rope chunk) into a ring of 16 KB slots, 128 bytes of 128 keys each, with cp.async;
-//  * warps 4..11 read the codes again (they are in L2 by then), widen them to
+//  * warps 4..7 read the codes again (they are in L2 by then), widen them to
 //    fp16 and store them for the value product: two slots of 128 keys x 128
 //    dims; at the start of a query row they prepare the query;
-//  * warps 12..19 are the softmax, two groups of 32 heads: a thread owns a key;
+//  * warps 8..15 are the softmax, two groups of 32 heads: a thread owns a key;
 //  * warp 2 issues S^T = K Q^T (M = 128 keys) one tile ahead of
 //    O^T += V^T P^T (M = 128 dims x 4, N = 64 heads).
 #pragma once
@@ -44,14 +44,19 @@ namespace dsa {
 
 namespace {
 
-constexpr int kPgThreads = 640;
-constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 12;  // first warp of each role (keys: 0)
+constexpr int kPgThreads = 512;
+constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 8;  // first warp of each role (keys: 0)
+constexpr int kPgRegs = 128;  // registers a thread at launch; then by warpgroup:
+constexpr int kPgRegs0 = 72, kPgRegsV = 136, kPgRegsS = 152;
+static_assert(kPgThreads * kPgRegs <= 65536 && 128 * (kPgRegs0 + kPgRegsV + 2 * kPgRegsS) <= kPgThreads * kPgRegs,
+              "the warpgroups' registers must not exceed the block's");
 constexpr int kPgSlot = 16384;        // 128 keys x 128 bytes, 128B-swizzled
 constexpr int kPgKSlots = 4;
 constexpr int kPgVSlots = 2;
 constexpr int kPgRows = 4;            // tiles whose row numbers are held
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
 constexpr float kPgShift = 6.f;       // log2 of the probability at the running maximum
+constexpr float kPgNone = 1e30f;      // shift of a head without a maximum yet: any finite score sets one
 
 constexpr int kPgQ8 = 0;                                     // 4 chunks of 128 rows (hi heads, lo heads) x 128 codes
 constexpr int kPgQR = kPgQ8 + 4 * kPgSlot;                   // 64 heads x 64 bf16
@@ -61,8 +66,8 @@ constexpr int kPgV = kPgK + kPgKSlots * kPgSlot;             // a slot: two chun
 constexpr int kPgRowOff = kPgV + kPgVSlots * 2 * kPgSlot;    // int row[kPgRows][128]
 constexpr int kPgScaleOff = kPgRowOff + kPgRows * 512;       // float 2^k[kPgRows][128]
 constexpr int kPgRedOff = kPgScaleOff + kPgRows * 512;       // float red[2][4][32]
-constexpr int kPgMOff = kPgRedOff + 1024;                    // float m[64], alpha[64], l[64], 2^e[2][64]
-constexpr int kPgBarOff = kPgMOff + 1280;
+constexpr int kPgMOff = kPgRedOff + 1024;                    // float m[64], alpha[64], l[64], 2^e[2][64], kPgShift - m [64]
+constexpr int kPgBarOff = kPgMOff + 1536;
 enum PgBar {
   kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarDrain, kBarSFull,  // s_full x2
   kBarKFull = kBarSFull + 2, kBarKEmpty = kBarKFull + kPgKSlots, kBarVFull = kBarKEmpty + kPgKSlots,
@@ -144,29 +149,42 @@ __device__ __forceinline__ long long tiles_of(int nq, long long len, int topk_ti
   return none + tiles_below(max(0ll, base + j)) - tiles_below(max(0ll, base));
 }
 
-// Lane L of the warp gets the reduction of v[L] over the 32 lanes.
+// Lane L of the warp gets the reduction of v[L % 16] over the 32 lanes.
 template <bool kMax>
-__device__ __forceinline__ float reduce_scatter32(const float (&v)[32]) {
+__device__ __forceinline__ float reduce_scatter16(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
-  float a[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float mine = (lane & 16) ? v[16 + i] : v[i], give = (lane & 16) ? v[i] : v[16 + i];
-    const float got = __shfl_xor_sync(0xffffffffu, give, 16);
-    a[i] = kMax ? fmax_(mine, got) : mine + got;
-  }
 #pragma unroll
   for (int w = 8; w >= 1; w >>= 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < w) {
-        const float mine = (lane & w) ? a[w + i] : a[i], give = (lane & w) ? a[i] : a[w + i];
-        const float got = __shfl_xor_sync(0xffffffffu, give, w);
-        a[i] = kMax ? fmax_(mine, got) : mine + got;
-      }
+    for (int i = 0; i < w; ++i) {
+      const float mine = (lane & w) ? v[w + i] : v[i], give = (lane & w) ? v[i] : v[w + i];
+      const float got = __shfl_xor_sync(0xffffffffu, give, w);
+      v[i] = kMax ? fmaxf(mine, got) : mine + got;
     }
   }
-  return a[0];
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+// Codes 16 g .. 16 g + 15 (+ col) of a thread's eight keys; zeros where there is no key.
+__device__ __forceinline__ void load_codes(uint4 (&w)[8], const int (&y)[8], const uint8_t* base, int col) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j] = y[j] >= 0 ? *reinterpret_cast<const uint4*>(base + (long long)y[j] * kRow8 + col) : make_uint4(0, 0, 0, 0);
+}
+
+// Sixteen codes as fp16, into two 16-byte segments.
+__device__ __forceinline__ void store_fp16(uint8_t* s0, uint8_t* s1, const uint4& x) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+  uint32_t f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(f[2 * i]), "=r"(f[2 * i + 1])
+        : "r"(xs[i]));
+  *reinterpret_cast<uint4*>(s0) = make_uint4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<uint4*>(s1) = make_uint4(f[4], f[5], f[6], f[7]);
 }
 
 template <bool kSparse>
@@ -185,6 +203,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   float* alpha_s = m_s + 64;
   float* l_s = m_s + 128;
   float* g_s = m_s + 192;  // two rows' worth: the next row's query is prepared while this one's scores are still read
+  float* off_s = m_s + 320;  // what a score is shifted by before 2^x: kPgShift - m, kPgNone before there is an m
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kPgTailOff + 4);
   int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile, tiles of this CTA, tiles of a share
@@ -192,7 +211,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int topk_tiles = kSparse ? (topk + 127) >> 7 : 0;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(kBarQFull), 256);
+    mbar_init(bar(kBarQFull), 128);
     mbar_init(bar(kBarQEmpty), 1);
     mbar_init(bar(kBarPFull), 256);
     mbar_init(bar(kBarPFree), 1);
@@ -205,12 +224,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(bar(kBarKEmpty + i), 1);
     }
     for (int i = 0; i < kPgVSlots; ++i) {
-      mbar_init(bar(kBarVFull + i), 256);
+      mbar_init(bar(kBarVFull + i), 128);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
     for (int i = 0; i < kPgRows; ++i) {
       mbar_init(bar(kBarRowFull + i), 1);
-      mbar_init(bar(kBarRowEmpty + i), 18);  // one per warp of the key, value and softmax roles
+      mbar_init(bar(kBarRowEmpty + i), 14);  // one per warp of the key, value and softmax roles
     }
     *abort_flag = 0;
     start_s[3] = 0;
@@ -285,245 +304,334 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
   if (!busy) {
     // nothing to do
-  } else if (warp < kPgMma) {
-    // ---------------------------------------------------------------- keys
-    const int g = threadIdx.x & 7, r0 = threadIdx.x >> 3;  // segment g of rows r0 + 8 j
-    const uint32_t off = uint32_t(r0 * 128 + ((g ^ r0) << 4));
-    int slot = 0;
-    uint32_t sphase = 0;
-    bool ok = true;
-    for (int n = 0; n < walk.left && ok; ++n) {
-      const int rb = n % kPgRows;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u, lim, abort_flag));
-      if (!ok) break;
-      const uint8_t* src[16];
-      uint32_t skip = 0;
+  } else if (warp < kPgVWarp) {
+    reg_dec<kPgRegs0>();
+    if (warp < kPgMma) {
+      // ---------------------------------------------------------------- keys
+      const int g = threadIdx.x & 7, r0 = threadIdx.x >> 3;  // segment g of rows r0 + 8 j
+      const uint32_t off = uint32_t(r0 * 128 + ((g ^ r0) << 4));
+      const uint8_t* base = c.kv8 + 16 * g;
+      int slot = 0;
+      uint32_t sphase = 0;
+      bool ok = true;
+      for (int n = 0; n < walk.left && ok; ++n) {
+        const int rb = n % kPgRows;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u, lim, abort_flag));
+        if (!ok) break;
+        int y[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int y = row_s[rb * 128 + r0 + 8 * j];
-        src[j] = c.kv8 + (long long)(y >= 0 ? y : 0) * kRow8 + g * 16;
-        skip |= (y < 0 ? 1u : 0u) << j;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
-      for (int ch = 0; ch < 5; ++ch) {
-        if (!(ok = mbar_wait(bar(kBarKEmpty + slot), sphase ^ 1u, lim, abort_flag))) break;
-        const uint32_t dst = sbase + kPgK + slot * kPgSlot + off;
+        for (int j = 0; j < 16; ++j) y[j] = row_s[rb * 128 + r0 + 8 * j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+        for (int ch = 0; ch < 5; ++ch) {
+          if (!(ok = mbar_wait(bar(kBarKEmpty + slot), sphase ^ 1u, lim, abort_flag))) break;
+          const uint32_t dst = sbase + kPgK + slot * kPgSlot + off;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) cp_async_16_or_zero(dst + j * 1024, src[j] + 128 * ch, (skip >> j) & 1u);
-        cp_async_arrive_noinc(bar(kBarKFull + slot));
-        if (++slot == kPgKSlots) {
-          slot = 0;
-          sphase ^= 1u;
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    cp_async_wait_all();
-  } else if (warp == kPgAddr) {
-    // ---------------------------------------------------------------- addresses
-    // Keys lane + 32 i of each tile.  Position, page and scale are three loads
-    // that follow from each other; each is made one tile after the one before it,
-    // so that none is waited for.
-    const int total = walk.left;
-    int s2[4], s1[4], page1[4], row0[4], b2;
-    float sc0[4];
-    auto position = [&]() {  // of the walk's next tile (-1: none); then step on
-      b2 = walk.b;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = walk.tile * 128 + lane + 32 * i;
-        int s = -1;
-        if (walk.left > 0) {
-          if (!kSparse) {
-            s = j < walk.seen ? j : -1;
-          } else if (j < topk) {
-            s = idx[(long long)walk.t * topk + j];
-            if (s >= walk.seen) {
-              raise_status(kStatusBadRow);
-              s = -1;
-            }
+          for (int j = 0; j < 16; ++j)
+            cp_async_16_or_zero(dst + j * 1024, base + (long long)max(y[j], 0) * kRow8 + 128 * ch, y[j] < 0);
+          cp_async_arrive_noinc(bar(kBarKFull + slot));
+          if (++slot == kPgKSlots) {
+            slot = 0;
+            sphase ^= 1u;
           }
         }
-        s2[i] = s;
+        ok = __all_sync(0xffffffffu, ok);
       }
-      if (walk.left > 0) walk.advance(1);
-    };
-    auto page = [&]() {
+      cp_async_wait_all();
+    } else if (warp == kPgAddr) {
+      // ---------------------------------------------------------------- addresses
+      // Keys lane + 32 i of each tile.  Position, page and scale are three loads
+      // that follow from each other; each is made one tile after the one before it,
+      // so that none is waited for.
+      const int total = walk.left;
+      int s2[4], s1[4], page1[4], row0[4], b2;
+      float sc0[4];
+      auto position = [&]() {  // of the walk's next tile (-1: none); then step on
+        b2 = walk.b;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s1[i] = s2[i];
-        page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + int(unsigned(s2[i]) / unsigned(c.page_size))] : 0;
-      }
-    };
-    auto scale = [&]() {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int y = -1;
-        if (s1[i] >= 0) {
-          if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + int(unsigned(s1[i]) % unsigned(c.page_size));
-          else raise_status(kStatusBadRow);
+        for (int i = 0; i < 4; ++i) {
+          const int j = walk.tile * 128 + lane + 32 * i;
+          int s = -1;
+          if (walk.left > 0) {
+            if (!kSparse) {
+              s = j < walk.seen ? j : -1;
+            } else if (j < topk) {
+              s = idx[(long long)walk.t * topk + j];
+              if (s >= walk.seen) {
+                raise_status(kStatusBadRow);
+                s = -1;
+              }
+            }
+          }
+          s2[i] = s;
         }
-        row0[i] = y;
-        sc0[i] = y >= 0 ? c.kv_scale[y] : 0.f;
-      }
-    };
-    position();
-    page();
-    position();
-    scale();
-    page();
-    position();
-    for (int n = 0; n < total; ++n) {
-      const int rb = n % kPgRows;
-      const bool ok = __all_sync(
-          0xffffffffu, mbar_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u, lim, abort_flag));
-      if (!ok) break;
+        if (walk.left > 0) walk.advance(1);
+      };
+      auto page = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        row_s[rb * 128 + lane + 32 * i] = row0[i];
-        scale_s[rb * 128 + lane + 32 * i] = sc0[i];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarRowFull + rb));
+        for (int i = 0; i < 4; ++i) {
+          s1[i] = s2[i];
+          page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + int(unsigned(s2[i]) / unsigned(c.page_size))] : 0;
+        }
+      };
+      auto scale = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int y = -1;
+          if (s1[i] >= 0) {
+            if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + int(unsigned(s1[i]) % unsigned(c.page_size));
+            else raise_status(kStatusBadRow);
+          }
+          row0[i] = y;
+          sc0[i] = y >= 0 ? c.kv_scale[y] : 0.f;
+        }
+      };
+      position();
+      page();
+      position();
       scale();
       page();
       position();
+      for (int n = 0; n < total; ++n) {
+        const int rb = n % kPgRows;
+        const bool ok = __all_sync(
+            0xffffffffu, mbar_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u, lim, abort_flag));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          row_s[rb * 128 + lane + 32 * i] = row0[i];
+          scale_s[rb * 128 + lane + 32 * i] = sc0[i];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarRowFull + rb));
+        scale();
+        page();
+        position();
+      }
+    } else {
+      // ---------------------------------------------------------------- MMA issuer
+      {
+        const bool el = elect_one();
+        const uint32_t idesc_k = idesc_e4m3(128, 128);
+        const uint32_t idesc_r = idesc_bf16(128, 64, 0, 0);
+        const uint32_t idesc_v = idesc_f16(128, 64, 1, 1);
+        int kslot = 0, vslot = 0, n = 0, seg = 0;  // n: the row's first tile
+        uint32_t kphase = 0, vphase = 0, cphase = 0;
+        bool ok = true;
+        auto warp_wait = [&](uint32_t b, uint32_t parity) {
+          return __all_sync(0xffffffffu, mbar_wait(b, parity, lim, abort_flag)) != 0;
+        };
+        auto next_k = [&]() {
+          if (el) mma_commit(bar(kBarKEmpty + kslot));
+          if (++kslot == kPgKSlots) {
+            kslot = 0;
+            kphase ^= 1u;
+          }
+        };
+        // S^T of the codes (N = 128, first) into buffer `buf`
+        auto codes = [&](int buf) {
+          for (int ch = 0; ch < 4; ++ch) {
+            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) return;
+            fence_proxy_async_smem();
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (el) mma_f8_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
+                        smem_desc(sbase + kPgQ8 + ch * kPgSlot + 32 * k, 16, 1024, kSwizzle128B), idesc_k,
+                        (ch | k) ? 1u : 0u);
+            next_k();
+          }
+          if (el) mma_commit(bar(kBarCodes));
+        };
+        // ... and of the rope half into the hi columns on top of it.  Only products of one shape and kind are ordered by
+        // their issue: a barrier stands between these two (and other work is queued meanwhile).
+        auto rope = [&](int buf) {
+          if (!(ok = warp_wait(bar(kBarCodes), cphase))) return;
+          cphase ^= 1u;
+          if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) return;
+          fence_proxy_async_smem();
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (el) mma_bf16_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
+                        smem_desc(sbase + kPgQR + 32 * k, 16, 1024, kSwizzle128B), idesc_r, 1u);
+          next_k();
+          if (el) mma_commit(bar(kBarSFull + buf));
+        };
+        while (ok && walk.left > 0) {
+          const int nt = walk.segment();
+          if (!(ok = warp_wait(bar(kBarQFull), uint32_t(seg & 1)))) break;
+          codes(n & 1);
+          for (int s = 0; s <= nt && ok; ++s) {
+            // scores of tile s, codes of tile s + 1, values of tile s - 1
+            if (s < nt) {
+              rope((n + s) & 1);
+              if (!ok) break;
+              if (s == nt - 1 && el) mma_commit(bar(kBarQEmpty));
+            }
+            if (s >= 1 && !(ok = warp_wait(bar(kBarPFull), uint32_t(n + s - 1) & 1u))) break;
+            // tile s + 1 takes the buffer of tile s - 1, whose probabilities are there
+            if (s + 1 < nt) codes((n + s + 1) & 1);
+            if (!ok || s == 0) continue;
+            if (s == 1 && seg > 0 && !(ok = warp_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u))) break;
+            tc_fence_after();
+            for (int m = 0; m < 4; ++m) {
+              if (!(ok = warp_wait(bar(kBarVFull + vslot), vphase))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (el)
+                  mma_bf16_ss(tmem + kPgOCol + 64 * m,
+                            smem_desc(sbase + kPgV + vslot * 2 * kPgSlot + k * 2048, kPgSlot, 1024, kSwizzle128B),
+                            smem_desc(sbase + kPgP + k * 2048, kPgSlot, 1024, kSwizzle128B), idesc_v,
+                            (s > 1 || k > 0) ? 1u : 0u);
+              if (el) mma_commit(bar(kBarVEmpty + vslot));
+              if (++vslot == kPgVSlots) {
+                vslot = 0;
+                vphase ^= 1u;
+              }
+            }
+            if (ok && el) mma_commit(bar(kBarPFree));
+          }
+          n += nt;
+          walk.advance(nt);
+          ++seg;
+        }
+        if (el) mma_commit(bar(kBarDrain));
+        mbar_drain(bar(kBarDrain), 0);
+      }
+      __syncwarp();
     }
-  } else if (warp >= kPgVWarp && warp < kPgSoft) {
+  } else if (warp < kPgSoft) {
+    reg_inc<kPgRegsV>();
     // ---------------------------------------------------------------- queries and values
     const int vt = threadIdx.x - 32 * kPgVWarp;
     const int vw = warp - kPgVWarp;
-    const int g = vt & 7, r0 = vt >> 3;  // codes 16 g .. 16 g + 15 of rows r0 + 32 j
+    // Codes 16 g .. 16 g + 15 of rows r0 + 16 j: segments 2 (g % 4) and the next of
+    // chunk g / 4 of the widened row.  Eight lanes take the first chunk of a row and
+    // the second of its neighbour: with the swizzle, their stores fill all banks.
+    const int g = vt & 7, r0 = (vt >> 3) ^ (g >> 2);
     const uint32_t voff = uint32_t((g >> 2) * kPgSlot + r0 * 128);
-    // two 16-byte segments of the widened row; lanes of the second chunk start with
-    // the other one, so that eight lanes fill all banks
-    const uint32_t seg0 = uint32_t(((2 * (g & 3) + (g >> 2)) ^ (r0 & 7)) << 4);
-    const uint32_t seg1 = uint32_t(((2 * (g & 3) + 1 - (g >> 2)) ^ (r0 & 7)) << 4);
-    int slot = 0, n = 0, seg = 0;
+    const uint32_t seg0 = uint32_t(((2 * (g & 3)) ^ (r0 & 7)) << 4), seg1 = seg0 ^ 16u;
+    const int total = walk.left;
+    int slot = 0, seg = 0, row_tiles = 0;
     uint32_t sphase = 0;
     bool ok = true;
-    while (ok && walk.left > 0) {
-      const int nt = walk.segment();
-      // --- the query row: hi and lo codes and the scaled rope half
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQEmpty), uint32_t(seg & 1) ^ 1u, lim, abort_flag));
-      if (!ok) break;
-#pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
-        const int h = vw * 8 + i;
-        const uint16_t* qh = q + ((long long)walk.t * 64 + h) * 576;
-        const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 16 * lane);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(qh + 16 * lane + 8);
-        const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
-        const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        uint32_t amax = 0;
-        auto see = [&](uint32_t bits) {
-          bits &= 0x7fffffffu;
-          if (bits < 0x7f800000u) amax = max(amax, bits);
-        };
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(b, parity, lim, abort_flag)) != 0;
+    };
+    // The codes of a slot are loaded two slots ahead, across tiles and rows.
+    const uint8_t* base = c.kv8 + 16 * g;
+    int y[8];
+    auto rows = [&](int n) {
+      const int rb = n % kPgRows;
+      if (!(ok = wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          see(w[j] << 16);
-          see(w[j] & 0xffff0000u);
-        }
-        see(xr << 16);
-        see(xr & 0xffff0000u);
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        // 2^e with max |q| <= 448 2^e
-        const int e0 = int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
-        const int e = max(e0, -100);
-        const float inv = pow2f(-e);
-        uint32_t hi[4], lo[4];
+      for (int j = 0; j < 8; ++j) y[j] = row_s[rb * 128 + r0 + 16 * j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+    };
+    uint4 w0[8], w1[8];
+    auto widen = [&](const uint4 (&w)[8]) {  // into the next slot
+      if (!wait(bar(kBarVEmpty + slot), sphase ^ 1u)) return false;
+      uint8_t* dst = smem + kPgV + slot * 2 * kPgSlot + voff;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[4] = {__uint_as_float(w[2 * j] << 16), __uint_as_float(w[2 * j] & 0xffff0000u),
-                        __uint_as_float(w[2 * j + 1] << 16), __uint_as_float(w[2 * j + 1] & 0xffff0000u)};
-          uint32_t hh = 0, ll = 0;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            float a = v[2 * p] * inv, bb = v[2 * p + 1] * inv;
-            // an infinite value is taken as NaN (codes have no infinity): so is every score with it
-            if (isinf(a)) a = __uint_as_float(0x7fc00000u);
-            if (isinf(bb)) bb = __uint_as_float(0x7fc00000u);
-            const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(a, bb), __NV_SATFINITE, __NV_E4M3);
-            const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c2, __NV_E4M3)));
-            const __nv_fp8x2_storage_t d2 =
-                __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (bb - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-            hh |= uint32_t(c2) << (16 * p);
-            ll |= uint32_t(d2) << (16 * p);
-          }
-          hi[j] = hh;
-          lo[j] = ll;
-        }
-        // lane holds codes 16 lane ..: chunk lane / 8, segment lane % 8
-        uint8_t* dst = smem + kPgQ8 + (lane >> 3) * kPgSlot + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + 64 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) =
-            __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
-        if (lane == 0) g_s[64 * (seg & 1) + h] = pow2f(e);
-      }
+      for (int j = 0; j < 8; ++j) store_fp16(dst + j * 2048 + seg0, dst + j * 2048 + seg1, w[j]);
       fence_proxy_async_smem();
-      mbar_arrive(bar(kBarQFull));
-      // --- the values of its tiles
-      for (int t = 0; t < nt && ok; ++t, ++n) {
-        const int rb = n % kPgRows;
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u, lim, abort_flag));
-        if (!ok) break;
-        const uint8_t* src[4];
-        bool has[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int y = row_s[rb * 128 + r0 + 32 * j];
-          has[j] = y >= 0;
-          src[j] = c.kv8 + (long long)(y >= 0 ? y : 0) * kRow8 + 16 * g;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
-        uint4 w[2][4];
-        auto load = [&](int m) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[m & 1][j] = has[j] ? *reinterpret_cast<const uint4*>(src[j] + 128 * m) : make_uint4(0, 0, 0, 0);
-        };
-        load(0);
-        load(1);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVEmpty + slot), sphase ^ 1u, lim, abort_flag));
-          if (ok) {
-            uint8_t* dst = smem + kPgV + slot * 2 * kPgSlot + voff;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 x = w[m & 1][j];
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-              uint32_t f[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __half2_raw h2 =
-                    __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(xs[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-                f[i] = uint32_t(h2.x) | (uint32_t(h2.y) << 16);
-              }
-              const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), bq = make_uint4(f[4], f[5], f[6], f[7]);
-              const bool sw = g >> 2;
-              *reinterpret_cast<uint4*>(dst + j * 4096 + seg0) = sw ? bq : a;
-              *reinterpret_cast<uint4*>(dst + j * 4096 + seg1) = sw ? a : bq;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(bar(kBarVFull + slot));
-            if (++slot == kPgVSlots) {
-              slot = 0;
-              sphase ^= 1u;
-            }
-            if (m < 2) load(m + 2);
-          }
-        }
+      mbar_arrive(bar(kBarVFull + slot));
+      if (++slot == kPgVSlots) {
+        slot = 0;
+        sphase ^= 1u;
       }
-      walk.advance(nt);
-      ++seg;
+      return true;
+    };
+    rows(0);
+    if (ok) {
+      load_codes(w0, y, base, 0);
+      load_codes(w1, y, base, 128);
     }
-  } else if (warp >= kPgSoft) {
+    for (int n = 0; n < total && ok; ++n) {
+      if (row_tiles == 0) {
+        // --- the query row: hi and lo codes and the scaled rope half
+        if (!(ok = wait(bar(kBarQEmpty), uint32_t(seg & 1) ^ 1u))) break;
+#pragma unroll 2
+        for (int i = 0; i < 16; ++i) {
+          const int h = vw * 16 + i;
+          const uint16_t* qh = q + ((long long)walk.t * 64 + h) * 576;
+          const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 16 * lane);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(qh + 16 * lane + 8);
+          const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
+          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          uint32_t amax = 0;
+          auto see = [&](uint32_t bits) {
+            bits &= 0x7fffffffu;
+            if (bits < 0x7f800000u) amax = max(amax, bits);
+          };
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            see(w[j] << 16);
+            see(w[j] & 0xffff0000u);
+          }
+          see(xr << 16);
+          see(xr & 0xffff0000u);
+          amax = __reduce_max_sync(0xffffffffu, amax);
+          // 2^e with max |q| <= 448 2^e
+          const int e0 = int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+          const int e = max(e0, -100);
+          const float inv = pow2f(-e);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v[4] = {__uint_as_float(w[2 * j] << 16), __uint_as_float(w[2 * j] & 0xffff0000u),
+                          __uint_as_float(w[2 * j + 1] << 16), __uint_as_float(w[2 * j + 1] & 0xffff0000u)};
+            uint32_t hh = 0, ll = 0;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              float a = v[2 * p] * inv, bb = v[2 * p + 1] * inv;
+              // an infinite value is taken as NaN (codes have no infinity): so is every score with it
+              if (isinf(a)) a = __uint_as_float(0x7fc00000u);
+              if (isinf(bb)) bb = __uint_as_float(0x7fc00000u);
+              const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(a, bb), __NV_SATFINITE, __NV_E4M3);
+              const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c2, __NV_E4M3)));
+              const __nv_fp8x2_storage_t d2 =
+                  __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (bb - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+              hh |= uint32_t(c2) << (16 * p);
+              ll |= uint32_t(d2) << (16 * p);
+            }
+            hi[j] = hh;
+            lo[j] = ll;
+          }
+          // lane holds codes 16 lane ..: chunk lane / 8, segment lane % 8
+          uint8_t* dst = smem + kPgQ8 + (lane >> 3) * kPgSlot + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + 64 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) =
+              __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
+          if (lane == 0) g_s[64 * (seg & 1) + h] = pow2f(e);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kBarQFull));
+        row_tiles = walk.segment();
+        walk.advance(row_tiles);
+        ++seg;
+      }
+      --row_tiles;
+      if (!(ok = widen(w0))) break;
+      load_codes(w0, y, base, 256);
+      if (!(ok = widen(w1))) break;
+      load_codes(w1, y, base, 384);
+      if (!(ok = widen(w0))) break;
+      const bool more = n + 1 < total;
+      if (more) {
+        rows(n + 1);
+        if (!ok) break;
+        load_codes(w0, y, base, 0);
+      }
+      if (!(ok = widen(w1))) break;
+      if (more) load_codes(w1, y, base, 128);
+    }
+  } else {
+    reg_inc<kPgRegsS>();
     // ---------------------------------------------------------------- softmax
     const int half = (warp - kPgSoft) >> 2;   // heads 32 half .. 32 half + 31
     const int quarter = warp & 3;             // TMEM lanes of this warp
@@ -542,10 +650,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int2 split = make_int2(-1, 0);
     while (ok && walk.left > 0) {
       const int nt = walk.segment();
-      float l_acc[32];
+      f32x2 l_acc[16];
 #pragma unroll
-      for (int h = 0; h < 32; ++h) l_acc[h] = 0.f;
-      if (st < 32) m_s[h0 + st] = -INFINITY;
+      for (int i = 0; i < 16; ++i) l_acc[i] = 0ull;
+      if (st < 32) {
+        m_s[h0 + st] = -INFINITY;
+        off_s[h0 + st] = kPgNone;
+      }
       for (int t = 0; t < nt && ok; ++t, ++n) {
         // (the barrier in here also publishes m_s; the scores' barrier follows the query's, so 2^e is there too)
         if (!(ok = wait_all(bar(kBarSFull + (n & 1)), uint32_t(n >> 1) & 1u))) break;
@@ -555,51 +666,66 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const float sc = scale_s[rb * 128 + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+        // Of this key (-inf without one) and 32 heads: x = y - m + kPgShift, y = S log2(e) + k.  k and m are whole
+        // numbers, so x takes one rounding, of its own size.  Above kPgShift + kLazyRescale for some head of some key
+        // (pass 0): the maxima of y (pass 1) give new m, and x is taken again (pass 2).
         const float cs = sc * scale_log2;
-        const float kf = float(int(__float_as_uint(sc) >> 23) - 127);
+        const float kf = valid ? float(int(__float_as_uint(sc) >> 23) - 127) : -INFINITY;
+        const f32x2 cs2 = f2_pack(cs, cs), kf2 = f2_pack(kf, kf), c16 = f2_pack(0.0625f, 0.0625f);
         const uint32_t sa = lane_addr + 128 * (n & 1) + h0;
-        // y of 16 heads from i0 on
-        auto scores = [&](int i0, float (&y)[16]) {
-          float lo[16];
-          tmem_ld16x2_sync(sa + i0, sa + 64 + i0, y, lo);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = fmaf(fmaf(lo[i], 0.0625f, y[i]), g_s[64 * (seg & 1) + h0 + i0 + i] * cs, kf);
-        };
-        int above = 0;
-#pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += 16) {
-          float y[16];
-          scores(i0, y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) above |= (valid && y[i] > m_s[h0 + i0 + i] + kLazyRescale) ? 1 : 0;
-        }
+        const ulonglong2* g4 = reinterpret_cast<const ulonglong2*>(g_s + 64 * (seg & 1) + h0);
+        const ulonglong2* off4 = reinterpret_cast<const ulonglong2*>(off_s + h0);
+        f32x2 x[16];
         int resc = 0;
-        if (bar_red_or(bar_id, 128, above)) {
-          float x[32];
-          {
-            float y[16];
-            scores(0, y);
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+          float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = valid ? y[i] : -INFINITY;
-            scores(16, y);
+          for (int i0 = 0; i0 < 16; i0 += 4) {
+            float hi[8], lo[8];
+            tmem_ld8x2_sync(sa + 2 * i0, sa + 64 + 2 * i0, hi, lo);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[16 + i] = valid ? y[i] : -INFINITY;
-          }
-          red[quarter * 32 + lane] = reduce_scatter32<true>(x);
-          named_bar_sync(bar_id, 128);
-          int mine = 0;
-          if (st < 32) {
-            const float mt = fmax_(fmax_(red[st], red[32 + st]), fmax_(red[64 + st], red[96 + st]));
-            const float mu = m_s[h0 + st];
-            float al = 1.f;
-            if (mt > mu + kLazyRescale) {
-              al = mu == -INFINITY ? 0.f : fast_exp2(mu - mt);
-              m_s[h0 + st] = mt;
-              mine = t > 0;
+            for (int i = 0; i < 4; i += 2) {
+              const ulonglong2 g = g4[(i0 + i) >> 1];
+              ulonglong2 off = off4[(i0 + i) >> 1];
+              if (pass == 1) off = make_ulonglong2(0ull, 0ull);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int k = i + e;
+                const f32x2 d = f2_fma(f2_pack(lo[2 * k], lo[2 * k + 1]), c16, f2_pack(hi[2 * k], hi[2 * k + 1]));
+                x[i0 + k] = f2_fma(d, f2_mul(e ? g.y : g.x, cs2), f2_add(kf2, e ? off.y : off.x));
+                float a0, a1;
+                f2_unpack(x[i0 + k], a0, a1);
+                top = fmaxf(top, fmaxf(a0, a1));
+              }
             }
-            alpha_s[h0 + st] = al;
           }
-          resc = bar_red_or(bar_id, 128, mine);  // also publishes m_s and alpha_s
+          if (pass == 0 && !bar_red_or(bar_id, 128, top > kPgShift + kLazyRescale ? 1 : 0)) break;
+          if (pass == 1) {
+#pragma unroll
+            for (int i0 = 0; i0 < 16; i0 += 8) {
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f2_unpack(x[i0 + i], v[2 * i], v[2 * i + 1]);
+              const float mx = reduce_scatter16<true>(v);
+              if (lane < 16) red[quarter * 32 + 2 * i0 + lane] = mx;
+            }
+            named_bar_sync(bar_id, 128);
+            int mine = 0;
+            if (st < 32) {
+              const float mt = floorf(fmaxf(fmaxf(red[st], red[32 + st]), fmaxf(red[64 + st], red[96 + st])));
+              const float mu = m_s[h0 + st];
+              float al = 1.f;
+              if (mt >= mu + kLazyRescale && mt > mu) {
+                al = mu == -INFINITY ? 0.f : fast_exp2(mu - mt);
+                m_s[h0 + st] = mt;
+                off_s[h0 + st] = kPgShift - mt;
+                mine = t > 0;
+              }
+              alpha_s[h0 + st] = al;
+            }
+            resc = bar_red_or(bar_id, 128, mine);  // also publishes m_s, off_s and alpha_s
+          }
         }
         // P and O are free once the previous value product is done
         if (t > 0 && !(ok = wait_all(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
@@ -617,31 +743,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           tmem_wait_st();
 #pragma unroll
-          for (int h = 0; h < 32; ++h) l_acc[h] *= alpha_s[h0 + h];
+          for (int i = 0; i < 16; ++i) l_acc[i] = f2_mul(l_acc[i], *reinterpret_cast<const f32x2*>(&alpha_s[h0 + 2 * i]));
         }
+        // u = 2^x, rounded to fp16 for the value product; the sums take it unrounded
         const float inv = valid ? pow2f(127 - int(__float_as_uint(sc) >> 23)) : 0.f;
+        const f32x2 inv2 = f2_pack(inv, inv);
         uint8_t* prow = smem + kPgP + r * 128;
 #pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += 16) {
-          float y[16];
-          scores(i0, y);
-          uint32_t w[8];
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+          uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float u[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float m = m_s[h0 + i0 + i + e];
-              // no finite maximum yet: nothing above -inf, or NaN, which stays NaN
-              u[e] = valid ? fast_exp2(y[i + e] - (m == -INFINITY ? 0.f : m) + kPgShift) : 0.f;
-              l_acc[i0 + i + e] = fmaf(u[e], inv, l_acc[i0 + i + e]);
-            }
-            const __half2 p = __floats2half2_rn(u[0], u[1]);
-            w[i >> 1] = *reinterpret_cast<const uint32_t*>(&p);
+          for (int i = 0; i < 4; ++i) {
+            float a0, a1;
+            f2_unpack(x[i0 + i], a0, a1);
+            a0 = fast_exp2(a0);
+            a1 = fast_exp2(a1);
+            l_acc[i0 + i] = f2_fma(f2_pack(a0, a1), inv2, l_acc[i0 + i]);
+            const __half2 p = __floats2half2_rn(a0, a1);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
           }
-          const int gg = (h0 + i0) >> 3;
-          *reinterpret_cast<uint4*>(prow + ((gg ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(prow + (((gg + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          *reinterpret_cast<uint4*>(prow + ((((h0 >> 3) + (i0 >> 2)) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -651,7 +772,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       // --- the row's (or the segment's) result
       if (!(ok = wait_all(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
       tc_fence_after();
-      red[quarter * 32 + lane] = reduce_scatter32<false>(l_acc);
+#pragma unroll
+      for (int i0 = 0; i0 < 16; i0 += 8) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f2_unpack(l_acc[i0 + i], v[2 * i], v[2 * i + 1]);
+        const float l = reduce_scatter16<false>(v);
+        if (lane < 16) red[quarter * 32 + 2 * i0 + lane] = l;
+      }
       named_bar_sync(bar_id, 128);
       if (st < 32) l_s[h0 + st] = red[st] + red[32 + st] + red[64 + st] + red[96 + st];
       named_bar_sync(bar_id, 128);
@@ -676,13 +804,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(kBarOFree));
       if (st < 32) {
-        const float l = l_s[h0 + st], m = m_s[h0 + st] - kPgShift;
+        const float l = l_s[h0 + st], m = m_s[h0 + st];  // (l is 0 or NaN where there is no m)
         if (!whole) {
-          prow[64 * 512 + h0 + st] = m_s[h0 + st];
+          prow[64 * 512 + h0 + st] = m;
           prow[64 * 512 + 64 + h0 + st] = l;
         } else if (lse) {
-          lse[(long long)walk.t * 64 + h0 + st] =
-              l == 0.f ? -INFINITY : ((m == -INFINITY ? -kPgShift : m) + log2f(l)) * 0.69314718055994531f;
+          lse[(long long)walk.t * 64 + h0 + st] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
         }
       }
       if (!whole && walk.tile == 0) {
@@ -694,94 +821,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       ++seg;
     }
     if (half == 0 && st == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
-  } else {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc_k = idesc_e4m3(128, 128);
-      const uint32_t idesc_r = idesc_bf16(128, 64, 0, 0);
-      const uint32_t idesc_v = idesc_f16(128, 64, 1, 1);
-      int kslot = 0, vslot = 0, n = 0, seg = 0;  // n: the row's first tile
-      uint32_t kphase = 0, vphase = 0, cphase = 0;
-      bool ok = true;
-      auto next_k = [&]() {
-        mma_commit(bar(kBarKEmpty + kslot));
-        if (++kslot == kPgKSlots) {
-          kslot = 0;
-          kphase ^= 1u;
-        }
-      };
-      // S^T of the codes (N = 128, first) into buffer `buf`
-      auto codes = [&](int buf) {
-        for (int ch = 0; ch < 4; ++ch) {
-          if (!(ok = mbar_wait(bar(kBarKFull + kslot), kphase, lim, abort_flag))) return;
-          fence_proxy_async_smem();
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f8_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
-                      smem_desc(sbase + kPgQ8 + ch * kPgSlot + 32 * k, 16, 1024, kSwizzle128B), idesc_k,
-                      (ch | k) ? 1u : 0u);
-          next_k();
-        }
-        mma_commit(bar(kBarCodes));
-      };
-      // ... and of the rope half into the hi columns on top of it.  Only products of one shape and kind are ordered by
-      // their issue: a barrier stands between these two (and other work is queued meanwhile).
-      auto rope = [&](int buf) {
-        if (!(ok = mbar_wait(bar(kBarCodes), cphase, lim, abort_flag))) return;
-        cphase ^= 1u;
-        if (!(ok = mbar_wait(bar(kBarKFull + kslot), kphase, lim, abort_flag))) return;
-        fence_proxy_async_smem();
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
-                      smem_desc(sbase + kPgQR + 32 * k, 16, 1024, kSwizzle128B), idesc_r, 1u);
-        next_k();
-        mma_commit(bar(kBarSFull + buf));
-      };
-      while (ok && walk.left > 0) {
-        const int nt = walk.segment();
-        if (!(ok = mbar_wait(bar(kBarQFull), uint32_t(seg & 1), lim, abort_flag))) break;
-        codes(n & 1);
-        for (int s = 0; s <= nt && ok; ++s) {
-          // scores of tile s, codes of tile s + 1, values of tile s - 1
-          if (s < nt) {
-            rope((n + s) & 1);
-            if (!ok) break;
-            if (s == nt - 1) mma_commit(bar(kBarQEmpty));
-          }
-          if (s >= 1 && !(ok = mbar_wait(bar(kBarPFull), uint32_t(n + s - 1) & 1u, lim, abort_flag))) break;
-          // tile s + 1 takes the buffer of tile s - 1, whose probabilities are there
-          if (s + 1 < nt) codes((n + s + 1) & 1);
-          if (!ok || s == 0) continue;
-          if (s == 1 && seg > 0 && !(ok = mbar_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u, lim, abort_flag))) break;
-          tc_fence_after();
-          for (int m = 0; m < 4; ++m) {
-            if (!(ok = mbar_wait(bar(kBarVFull + vslot), vphase, lim, abort_flag))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ss(tmem + kPgOCol + 64 * m,
-                          smem_desc(sbase + kPgV + vslot * 2 * kPgSlot + k * 2048, kPgSlot, 1024, kSwizzle128B),
-                          smem_desc(sbase + kPgP + k * 2048, kPgSlot, 1024, kSwizzle128B), idesc_v,
-                          (s > 1 || k > 0) ? 1u : 0u);
-            mma_commit(bar(kBarVEmpty + vslot));
-            if (++vslot == kPgVSlots) {
-              vslot = 0;
-              vphase ^= 1u;
-            }
-          }
-          if (ok) mma_commit(bar(kBarPFree));
-        }
-        n += nt;
-        walk.advance(nt);
-        ++seg;
-      }
-      mma_commit(bar(kBarDrain));
-      mbar_drain(bar(kBarDrain), 0);
-    }
-    __syncwarp();
   }
   pdl_trigger();
   tc_fence_before();
