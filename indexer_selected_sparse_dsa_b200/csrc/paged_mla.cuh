@@ -19,18 +19,26 @@
 // fp16 cannot hold is 2^-31 of the largest; sum u code is the numerator,
 // sum u 2^-k_s (fp32, u before rounding) the denominator.
 //
+// Shared memory carries no query: hi and lo lie in tensor memory as the A operand
+// (lanes 0..15 of each quarter the hi codes of 16 heads, lanes 16..31 their lo
+// codes), the keys are the B operand, and S comes out with a lane per head.  One
+// 16x32bx2 load then hands a thread the hi sums of its head, another the lo sums
+// of the same keys: maximum, sum and scale of a head are registers, not a reduction
+// over threads.  What is left in shared memory a tile: the codes once in (80 KB),
+// once out, the widened values in (128 KB) and out, and P.
+//
 // One CTA walks an equal share of all 128-key tiles of the batch, query row
 // after query row; a row that ends in another CTA leaves partial sums that
-// paged_mla_merge_kernel joins.  16 warps:
+// paged_mla_merge_kernel joins.  20 warps:
 //  * warp 3 finds each key's cache row and 2^k, up to four tiles ahead;
-//  * warps 0 and 1 copy the tile's rows (four chunks of 128 codes, then
-//    the rope chunk) into a ring of 16 KB slots, 128 bytes of 128 keys each, with cp.async;
-//  * warps 4..7 read the codes again (they are in L2 by then), widen them to
-//    fp16 and store them for the value product: two slots of 128 keys x 128
-//    dims; at the start of a query row they prepare the query;
-//  * warps 8..15 are the softmax, two groups of 32 heads: a thread owns a key;
-//  * warp 2 issues S^T = K Q^T (M = 128 keys) one tile ahead of
-//    O^T += V^T P^T (M = 128 dims x 4, N = 64 heads).
+//  * warps 0 and 1 copy the tile's rows (four chunks of 128 codes, then the rope
+//    chunk) into a ring of 16 KB slots, 128 bytes of 128 keys each, with cp.async;
+//  * warps 4..11 read the codes again (they are in L2 by then), widen them to
+//    fp16 and store them for the value product: two slots of 128 keys x 128 dims;
+//  * warps 12..19 are the softmax (a thread: one head, 32 keys) and prepare the
+//    next row's query while the last value product of a row runs;
+//  * warp 2 issues S = Q K^T (M = 64 heads x (hi, lo), N = 128 keys) one tile
+//    ahead of O^T += V^T P^T (M = 128 dims x 4, N = 64 heads).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,40 +52,34 @@ namespace dsa {
 
 namespace {
 
-constexpr int kPgThreads = 512;
-constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 8;  // first warp of each role (keys: 0)
-constexpr int kPgRegs = 128;  // registers a thread at launch; then by warpgroup:
-constexpr int kPgRegs0 = 72, kPgRegsV = 136, kPgRegsS = 152;
-static_assert(kPgThreads * kPgRegs <= 65536 && 128 * (kPgRegs0 + kPgRegsV + 2 * kPgRegsS) <= kPgThreads * kPgRegs,
-              "the warpgroups' registers must not exceed the block's");
+constexpr int kPgThreads = 640;       // five warps per scheduler: 96 registers a thread
+constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 12;  // first warp of each role (keys: 0)
 constexpr int kPgSlot = 16384;        // 128 keys x 128 bytes, 128B-swizzled
-constexpr int kPgKSlots = 4;
+constexpr int kPgKSlots = 7;
 constexpr int kPgVSlots = 2;
-constexpr int kPgRows = 4;            // tiles whose row numbers are held
+constexpr int kPgRows = 4;            // tiles whose keys are described
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
 constexpr float kPgShift = 6.f;       // log2 of the probability at the running maximum
 constexpr float kPgNone = 1e30f;      // shift of a head without a maximum yet: any finite score sets one
 
-constexpr int kPgQ8 = 0;                                     // 4 chunks of 128 rows (hi heads, lo heads) x 128 codes
-constexpr int kPgQR = kPgQ8 + 4 * kPgSlot;                   // 64 heads x 64 bf16
-constexpr int kPgP = kPgQR + 8192;                           // 128 keys x 64 heads fp16
+constexpr int kPgQR = 0;                                     // the query's rope half: 128 rows (hi rows; lo rows are 0) x 64 bf16
+constexpr int kPgP = kPgQR + kPgSlot;                        // 2 chunks of 64 heads x 64 keys fp16
 constexpr int kPgK = kPgP + kPgSlot;
 constexpr int kPgV = kPgK + kPgKSlots * kPgSlot;             // a slot: two chunks of 128 keys x 64 dims fp16
-constexpr int kPgRowOff = kPgV + kPgVSlots * 2 * kPgSlot;    // int row[kPgRows][128]
-constexpr int kPgScaleOff = kPgRowOff + kPgRows * 512;       // float 2^k[kPgRows][128]
-constexpr int kPgRedOff = kPgScaleOff + kPgRows * 512;       // float red[2][4][32]
-constexpr int kPgMOff = kPgRedOff + 1024;                    // float m[64], alpha[64], l[64], 2^e[2][64], kPgShift - m [64]
-constexpr int kPgBarOff = kPgMOff + 1536;
+constexpr int kPgKeyOff = kPgV + kPgVSlots * 2 * kPgSlot;    // of 128 keys: int row, float 2^k scale log2(e), k, 2^-k
+constexpr int kPgRedOff = kPgKeyOff + kPgRows * 2048;        // float red[2][64]
+constexpr int kPgMOff = kPgRedOff + 512;                     // float m[64], alpha[64], l[64], 2^e[64]
+constexpr int kPgBarOff = kPgMOff + 1024;
 enum PgBar {
-  kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarDrain, kBarSFull,  // s_full x2
-  kBarKFull = kBarSFull + 2, kBarKEmpty = kBarKFull + kPgKSlots, kBarVFull = kBarKEmpty + kPgKSlots,
+  kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarSFull, kBarSFree, kBarDrain,
+  kBarKFull, kBarKEmpty = kBarKFull + kPgKSlots, kBarVFull = kBarKEmpty + kPgKSlots,
   kBarVEmpty = kBarVFull + kPgVSlots, kBarRowFull = kBarVEmpty + kPgVSlots, kBarRowEmpty = kBarRowFull + kPgRows,
   kPgBars = kBarRowEmpty + kPgRows
 };
-constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, abort flag, start (b, t, tile), share
+constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, abort flag, start (b, t, tile, tiles), share
 constexpr int kPgSmem = kPgTailOff + 64;
 constexpr int kPgSmemAlloc = kPgSmem + 1024;
-constexpr uint32_t kPgOCol = 256;                            // S^T: two buffers of 128 columns; O^T: 4 x 64
+constexpr uint32_t kPgQCol = 128, kPgOCol = 256;             // S: 128 columns; Q: 128 (512 codes); O^T: 4 x 64
 
 // Query rows of sequence b: 0 (and the status bit) where cu_q is not in order.
 __device__ __forceinline__ int seq_rows(const int32_t* __restrict__ cu_q, int T, int b, int& q0, bool report) {
@@ -149,27 +151,10 @@ __device__ __forceinline__ long long tiles_of(int nq, long long len, int topk_ti
   return none + tiles_below(max(0ll, base + j)) - tiles_below(max(0ll, base));
 }
 
-// Lane L of the warp gets the reduction of v[L % 16] over the 32 lanes.
-template <bool kMax>
-__device__ __forceinline__ float reduce_scatter16(float (&v)[16]) {
-  const int lane = threadIdx.x & 31;
+// Codes 16 g .. 16 g + 15 (+ col) of a thread's four keys; zeros where there is no key.
+__device__ __forceinline__ void load_codes(uint4 (&w)[4], const int (&y)[4], const uint8_t* base, int col) {
 #pragma unroll
-  for (int w = 8; w >= 1; w >>= 1) {
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float mine = (lane & w) ? v[w + i] : v[i], give = (lane & w) ? v[i] : v[w + i];
-      const float got = __shfl_xor_sync(0xffffffffu, give, w);
-      v[i] = kMax ? fmaxf(mine, got) : mine + got;
-    }
-  }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
-}
-
-// Codes 16 g .. 16 g + 15 (+ col) of a thread's eight keys; zeros where there is no key.
-__device__ __forceinline__ void load_codes(uint4 (&w)[8], const int (&y)[8], const uint8_t* base, int col) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 4; ++j)
     w[j] = y[j] >= 0 ? *reinterpret_cast<const uint4*>(base + (long long)y[j] * kRow8 + col) : make_uint4(0, 0, 0, 0);
 }
 
@@ -187,23 +172,40 @@ __device__ __forceinline__ void store_fp16(uint8_t* s0, uint8_t* s1, const uint4
   *reinterpret_cast<uint4*>(s1) = make_uint4(f[4], f[5], f[6], f[7]);
 }
 
+// Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.  An infinite value
+// becomes NaN (codes have no infinity), and with it every score of the head.
+__device__ __forceinline__ void split_codes(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
+  const uint32_t w[2] = {w0, w1};
+  hi = lo = 0;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float a = __uint_as_float(w[p] << 16) * inv, b = __uint_as_float(w[p] & 0xffff0000u) * inv;
+    if (isinf(a)) a = __uint_as_float(0x7fc00000u);
+    if (isinf(b)) b = __uint_as_float(0x7fc00000u);
+    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3)));
+    const uint32_t d =
+        __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (b - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+    hi |= c << (16 * p);
+    lo |= d << (16 * p);
+  }
+}
+
 template <bool kSparse>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_mla_kernel(const uint16_t* __restrict__ q, int T, const int32_t* __restrict__ cu_q,
                      const int32_t* __restrict__ seq_len, const int32_t* __restrict__ idx, int topk,
                      const __grid_constant__ PagedCache c, float scale_log2, __nv_bfloat16* __restrict__ o_lat,
-                     float* __restrict__ lse, int2* __restrict__ meta, float* __restrict__ part, WaitLimit lim) {
+                     float* __restrict__ lse, int2* __restrict__ meta, float* __restrict__ part_out, WaitLimit lim) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + kPgBarOff + 8u * i; };
-  int* row_s = reinterpret_cast<int*>(smem + kPgRowOff);
-  float* scale_s = reinterpret_cast<float*>(smem + kPgScaleOff);
+  auto keys_of = [&](int n) { return smem + kPgKeyOff + (n % kPgRows) * 2048; };  // the table of the CTA's tile n
   float* m_s = reinterpret_cast<float*>(smem + kPgMOff);
   float* alpha_s = m_s + 64;
   float* l_s = m_s + 128;
-  float* g_s = m_s + 192;  // two rows' worth: the next row's query is prepared while this one's scores are still read
-  float* off_s = m_s + 320;  // what a score is shifted by before 2^x: kPgShift - m, kPgNone before there is an m
+  float* g_s = m_s + 192;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kPgTailOff + 4);
   int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile, tiles of this CTA, tiles of a share
@@ -211,25 +213,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int topk_tiles = kSparse ? (topk + 127) >> 7 : 0;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(kBarQFull), 128);
+    mbar_init(bar(kBarQFull), 8);  // one arrival per warp of the role, where several arrive
     mbar_init(bar(kBarQEmpty), 1);
-    mbar_init(bar(kBarPFull), 256);
+    mbar_init(bar(kBarPFull), 8);
     mbar_init(bar(kBarPFree), 1);
-    mbar_init(bar(kBarOFree), 256);
+    mbar_init(bar(kBarOFree), 8);
     mbar_init(bar(kBarCodes), 1);
+    mbar_init(bar(kBarSFull), 1);
+    mbar_init(bar(kBarSFree), 8);
     mbar_init(bar(kBarDrain), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(kBarSFull + i), 1);
     for (int i = 0; i < kPgKSlots; ++i) {
-      mbar_init(bar(kBarKFull + i), 64);
+      mbar_init(bar(kBarKFull + i), 64);  // every copying thread
       mbar_init(bar(kBarKEmpty + i), 1);
     }
     for (int i = 0; i < kPgVSlots; ++i) {
-      mbar_init(bar(kBarVFull + i), 128);
+      mbar_init(bar(kBarVFull + i), 8);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
     for (int i = 0; i < kPgRows; ++i) {
       mbar_init(bar(kBarRowFull + i), 1);
-      mbar_init(bar(kBarRowEmpty + i), 14);  // one per warp of the key, value and softmax roles
+      mbar_init(bar(kBarRowEmpty + i), 18);  // the key, value and softmax warps
     }
     *abort_flag = 0;
     start_s[3] = 0;
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
   // ---------------------------------------------------------------- this CTA's share
   {
-    long long* sums = reinterpret_cast<long long*>(smem);  // the warps' sums, in the query's room
+    long long* sums = reinterpret_cast<long long*>(smem);  // the warps' sums, in the rope half's room
     const int per = (c.batch + kPgThreads - 1) / kPgThreads;
     const int b0 = min(int(threadIdx.x) * per, c.batch), b1 = min(b0 + per, c.batch);
     auto weight = [&](int b, int& q0, int& nq, long long& len, bool report) {
@@ -302,525 +305,535 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   if (busy) walk.start(start_s);
   else if (threadIdx.x == 0) meta[blockIdx.x] = make_int2(-1, 0);
 
+  // A bounded wait of a whole warp, short in code (see the rolled loops of the
+  // issuing warp); the lanes agree on its outcome.
+  auto warp_wait = [&](uint32_t b, uint32_t parity) {
+    bool done = mbar_try_wait(b, parity);
+    if (!done) {
+      const unsigned long long t0 = globaltimer();
+#pragma unroll 1
+      do {
+        done = mbar_try_wait(b, parity);
+      } while (!done && !*abort_flag && globaltimer() - t0 <= lim.ns);
+    }
+    done = __all_sync(0xffffffffu, done);
+    if (!done) {
+      if (lane == 0 && !*abort_flag) raise_status(kStatusTimeout);
+      *abort_flag = 1;
+    }
+    return done;
+  };
+  // The same for a role of 256 threads: one warp tries, the others stand at a
+  // barrier, where they take no issue slots (a try that fails comes back in some
+  // 20 cycles).  The barrier hands everyone the outcome.
+  auto group_wait = [&](int id, int leader, uint32_t b, uint32_t parity) {
+    const bool done = warp == leader ? warp_wait(b, parity) : true;
+    return bar_red_or(id, 256, done ? 0 : 1) == 0;
+  };
   if (!busy) {
     // nothing to do
-  } else if (warp < kPgVWarp) {
-    reg_dec<kPgRegs0>();
-    if (warp < kPgMma) {
-      // ---------------------------------------------------------------- keys
-      const int g = threadIdx.x & 7, r0 = threadIdx.x >> 3;  // segment g of rows r0 + 8 j
-      const uint32_t off = uint32_t(r0 * 128 + ((g ^ r0) << 4));
-      const uint8_t* base = c.kv8 + 16 * g;
-      int slot = 0;
-      uint32_t sphase = 0;
-      bool ok = true;
-      for (int n = 0; n < walk.left && ok; ++n) {
-        const int rb = n % kPgRows;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u, lim, abort_flag));
-        if (!ok) break;
-        int y[16];
+  } else if (warp < kPgMma) {
+    // ---------------------------------------------------------------- keys
+    const int g = threadIdx.x & 7, r0 = threadIdx.x >> 3;  // segment g of rows r0 + 8 j
+    const uint32_t off = uint32_t(r0 * 128 + ((g ^ r0) << 4));
+    const uint8_t* base = c.kv8 + 16 * g;
+    int slot = 0;
+    uint32_t sphase = 0;
+    bool ok = true;
+    for (int n = 0; n < walk.left && ok; ++n) {
+      const int rb = n % kPgRows;
+      if (!(ok = warp_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) break;
+      int y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = row_s[rb * 128 + r0 + 8 * j];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
-        for (int ch = 0; ch < 5; ++ch) {
-          if (!(ok = mbar_wait(bar(kBarKEmpty + slot), sphase ^ 1u, lim, abort_flag))) break;
-          const uint32_t dst = sbase + kPgK + slot * kPgSlot + off;
+      for (int j = 0; j < 16; ++j) y[j] = reinterpret_cast<const int*>(keys_of(n))[r0 + 8 * j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+      for (int ch = 0; ch < 5; ++ch) {
+        if (!(ok = warp_wait(bar(kBarKEmpty + slot), sphase ^ 1u))) break;
+        const uint32_t dst = sbase + kPgK + slot * kPgSlot + off;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            cp_async_16_or_zero(dst + j * 1024, base + (long long)max(y[j], 0) * kRow8 + 128 * ch, y[j] < 0);
-          cp_async_arrive_noinc(bar(kBarKFull + slot));
-          if (++slot == kPgKSlots) {
-            slot = 0;
-            sphase ^= 1u;
-          }
+        for (int j = 0; j < 16; ++j)
+          cp_async_16_or_zero(dst + j * 1024, base + (long long)max(y[j], 0) * kRow8 + 128 * ch, y[j] < 0);
+        cp_async_arrive_noinc(bar(kBarKFull + slot));
+        if (++slot == kPgKSlots) {
+          slot = 0;
+          sphase ^= 1u;
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
-      cp_async_wait_all();
-    } else if (warp == kPgAddr) {
-      // ---------------------------------------------------------------- addresses
-      // Keys lane + 32 i of each tile.  Position, page and scale are three loads
-      // that follow from each other; each is made one tile after the one before it,
-      // so that none is waited for.
-      const int total = walk.left;
-      int s2[4], s1[4], page1[4], row0[4], b2;
-      float sc0[4];
-      auto position = [&]() {  // of the walk's next tile (-1: none); then step on
-        b2 = walk.b;
+    }
+    cp_async_wait_all();
+  } else if (warp == kPgAddr) {
+    // ---------------------------------------------------------------- addresses
+    // Keys lane + 32 i of each tile.  Position, page and scale are three loads
+    // that follow from each other; each is made one tile after the one before it,
+    // so that none is waited for.
+    const int total = walk.left;
+    int s2[4], s1[4], page1[4], row0[4], b2;
+    float sc0[4];
+    int seen_row = -1;
+    auto position = [&]() {  // of the walk's next tile (-1: none); then step on
+      b2 = walk.b;
+      if (walk.left > 0 && walk.t != seen_row) {  // a new row: its query is wanted soon
+        seen_row = walk.t;
+        const char* qr = reinterpret_cast<const char*>(q + (long long)walk.t * 64 * 576);
+        for (int i = lane; i < 64 * 576 * 2 / 128; i += 32) prefetch_l2(qr + 128 * i);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = walk.tile * 128 + lane + 32 * i;
-          int s = -1;
-          if (walk.left > 0) {
-            if (!kSparse) {
-              s = j < walk.seen ? j : -1;
-            } else if (j < topk) {
-              s = idx[(long long)walk.t * topk + j];
-              if (s >= walk.seen) {
-                raise_status(kStatusBadRow);
-                s = -1;
-              }
+      for (int i = 0; i < 4; ++i) {
+        const int j = walk.tile * 128 + lane + 32 * i;
+        int s = -1;
+        if (walk.left > 0) {
+          if (!kSparse) {
+            s = j < walk.seen ? j : -1;
+          } else if (j < topk) {
+            s = idx[(long long)walk.t * topk + j];
+            if (s >= walk.seen) {
+              raise_status(kStatusBadRow);
+              s = -1;
             }
           }
-          s2[i] = s;
         }
-        if (walk.left > 0) walk.advance(1);
-      };
-      auto page = [&]() {
+        s2[i] = s;
+      }
+      if (walk.left > 0) walk.advance(1);
+    };
+    auto page = [&]() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s1[i] = s2[i];
-          page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + int(unsigned(s2[i]) / unsigned(c.page_size))] : 0;
-        }
-      };
-      auto scale = [&]() {
+      for (int i = 0; i < 4; ++i) {
+        s1[i] = s2[i];
+        page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + int(unsigned(s2[i]) / unsigned(c.page_size))] : 0;
+      }
+    };
+    auto scale = [&]() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int y = -1;
-          if (s1[i] >= 0) {
-            if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + int(unsigned(s1[i]) % unsigned(c.page_size));
-            else raise_status(kStatusBadRow);
-          }
-          row0[i] = y;
-          sc0[i] = y >= 0 ? c.kv_scale[y] : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        int y = -1;
+        if (s1[i] >= 0) {
+          if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + int(unsigned(s1[i]) % unsigned(c.page_size));
+          else raise_status(kStatusBadRow);
         }
-      };
-      position();
-      page();
-      position();
+        row0[i] = y;
+        sc0[i] = y >= 0 ? c.kv_scale[y] : 0.f;
+      }
+    };
+    position();
+    page();
+    position();
+    scale();
+    page();
+    position();
+    for (int n = 0; n < total; ++n) {
+      const int rb = n % kPgRows;
+      if (!warp_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u)) break;
+      int* row_s = reinterpret_cast<int*>(keys_of(n)) + lane;
+      float* cs_s = reinterpret_cast<float*>(row_s) + 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = int(__float_as_uint(sc0[i]) >> 23);  // k + 127
+        const bool has = row0[i] >= 0;
+        row_s[32 * i] = row0[i];
+        cs_s[32 * i] = sc0[i] * scale_log2;
+        cs_s[128 + 32 * i] = has ? float(e - 127) : -INFINITY;
+        cs_s[256 + 32 * i] = has ? pow2f(127 - e) : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarRowFull + rb));
       scale();
       page();
       position();
-      for (int n = 0; n < total; ++n) {
-        const int rb = n % kPgRows;
-        const bool ok = __all_sync(
-            0xffffffffu, mbar_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u, lim, abort_flag));
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          row_s[rb * 128 + lane + 32 * i] = row0[i];
-          scale_s[rb * 128 + lane + 32 * i] = sc0[i];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarRowFull + rb));
-        scale();
-        page();
-        position();
-      }
-    } else {
-      // ---------------------------------------------------------------- MMA issuer
-      {
-        const bool el = elect_one();
-        const uint32_t idesc_k = idesc_e4m3(128, 128);
-        const uint32_t idesc_r = idesc_bf16(128, 64, 0, 0);
-        const uint32_t idesc_v = idesc_f16(128, 64, 1, 1);
-        int kslot = 0, vslot = 0, n = 0, seg = 0;  // n: the row's first tile
-        uint32_t kphase = 0, vphase = 0, cphase = 0;
-        bool ok = true;
-        auto warp_wait = [&](uint32_t b, uint32_t parity) {
-          return __all_sync(0xffffffffu, mbar_wait(b, parity, lim, abort_flag)) != 0;
-        };
-        auto next_k = [&]() {
-          if (el) mma_commit(bar(kBarKEmpty + kslot));
-          if (++kslot == kPgKSlots) {
-            kslot = 0;
-            kphase ^= 1u;
-          }
-        };
-        // S^T of the codes (N = 128, first) into buffer `buf`
-        auto codes = [&](int buf) {
+    }
+  } else if (warp == kPgMma) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t el = elect_one();
+    const uint32_t idesc_k = idesc_e4m3(128, 128);
+    const uint32_t idesc_r = idesc_bf16(128, 128, 0, 0);
+    const uint32_t idesc_v = idesc_f16(128, 64, 1, 0);
+    const uint64_t qr_desc = smem_desc(sbase + kPgQR, 16, 1024, kSwizzle128B);
+    const uint64_t p_desc = smem_desc(sbase + kPgP, 16, 1024, kSwizzle128B);
+    int kslot = 0, vslot = 0, n = 0, seg = 0;  // n: tiles whose scores are issued
+    uint32_t kphase = 0, vphase = 0;
+    bool ok = true;
+    // (the loops below stay rolled: five warps of four roles share a scheduler's instruction cache)
+    while (ok && walk.left > 0) {
+      const int nt = walk.segment();
+      if (!(ok = warp_wait(bar(kBarQFull), uint32_t(seg & 1)))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int t = -1; t < nt && ok; ++t) {  // scores of tile t + 1, values of tile t
+        const bool more = t + 1 < nt;
+        if (more) {
+          // S of the codes; the buffer is free once the softmax has read the tile before
+          if (n > 0 && !(ok = warp_wait(bar(kBarSFree), uint32_t(n - 1) & 1u))) break;
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
-            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) return;
+            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) break;
             fence_proxy_async_smem();
             tc_fence_after();
+            const uint64_t kd = smem_desc(sbase + kPgK + kslot * kPgSlot, 16, 1024, kSwizzle128B);
+            const uint32_t qa = tmem + kPgQCol + 32 * ch;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (el) mma_f8_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
-                        smem_desc(sbase + kPgQ8 + ch * kPgSlot + 32 * k, 16, 1024, kSwizzle128B), idesc_k,
-                        (ch | k) ? 1u : 0u);
-            next_k();
-          }
-          if (el) mma_commit(bar(kBarCodes));
-        };
-        // ... and of the rope half into the hi columns on top of it.  Only products of one shape and kind are ordered by
-        // their issue: a barrier stands between these two (and other work is queued meanwhile).
-        auto rope = [&](int buf) {
-          if (!(ok = warp_wait(bar(kBarCodes), cphase))) return;
-          cphase ^= 1u;
-          if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) return;
-          fence_proxy_async_smem();
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (el) mma_bf16_ss(tmem + 128 * buf, smem_desc(sbase + kPgK + kslot * kPgSlot + 32 * k, 16, 1024, kSwizzle128B),
-                        smem_desc(sbase + kPgQR + 32 * k, 16, 1024, kSwizzle128B), idesc_r, 1u);
-          next_k();
-          if (el) mma_commit(bar(kBarSFull + buf));
-        };
-        while (ok && walk.left > 0) {
-          const int nt = walk.segment();
-          if (!(ok = warp_wait(bar(kBarQFull), uint32_t(seg & 1)))) break;
-          codes(n & 1);
-          for (int s = 0; s <= nt && ok; ++s) {
-            // scores of tile s, codes of tile s + 1, values of tile s - 1
-            if (s < nt) {
-              rope((n + s) & 1);
-              if (!ok) break;
-              if (s == nt - 1 && el) mma_commit(bar(kBarQEmpty));
+            for (int k = 0; k < 4; ++k) mma_f8_ts_in(el, tmem, qa + 8 * k, kd + 2 * k, idesc_k, (ch | k) ? 1u : 0u);
+            mma_commit_in(el, bar(kBarKEmpty + kslot));
+            if (++kslot == kPgKSlots) {
+              kslot = 0;
+              kphase ^= 1u;
             }
-            if (s >= 1 && !(ok = warp_wait(bar(kBarPFull), uint32_t(n + s - 1) & 1u))) break;
-            // tile s + 1 takes the buffer of tile s - 1, whose probabilities are there
-            if (s + 1 < nt) codes((n + s + 1) & 1);
-            if (!ok || s == 0) continue;
-            if (s == 1 && seg > 0 && !(ok = warp_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u))) break;
-            tc_fence_after();
-            for (int m = 0; m < 4; ++m) {
-              if (!(ok = warp_wait(bar(kBarVFull + vslot), vphase))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (el)
-                  mma_bf16_ss(tmem + kPgOCol + 64 * m,
-                            smem_desc(sbase + kPgV + vslot * 2 * kPgSlot + k * 2048, kPgSlot, 1024, kSwizzle128B),
-                            smem_desc(sbase + kPgP + k * 2048, kPgSlot, 1024, kSwizzle128B), idesc_v,
-                            (s > 1 || k > 0) ? 1u : 0u);
-              if (el) mma_commit(bar(kBarVEmpty + vslot));
-              if (++vslot == kPgVSlots) {
-                vslot = 0;
-                vphase ^= 1u;
-              }
-            }
-            if (ok && el) mma_commit(bar(kBarPFree));
           }
-          n += nt;
-          walk.advance(nt);
-          ++seg;
+          if (!ok) break;
+          mma_commit_in(el, bar(kBarCodes));
+        } else {
+          mma_commit_in(el, bar(kBarQEmpty));
         }
-        if (el) mma_commit(bar(kBarDrain));
-        mbar_drain(bar(kBarDrain), 0);
+        if (t >= 0) {
+          if (!(ok = warp_wait(bar(kBarPFull), uint32_t(n - 1) & 1u))) break;
+          if (t == 0 && seg > 0 && !(ok = warp_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u))) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          if (t >= 0) {  // 128 dims of the value product
+            if (!(ok = warp_wait(bar(kBarVFull + vslot), vphase))) break;
+            tc_fence_after();
+            const uint64_t vd = smem_desc(sbase + kPgV + vslot * 2 * kPgSlot, kPgSlot, 1024, kSwizzle128B);
+            const uint32_t od = tmem + kPgOCol + 64 * m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ss_in(el, od, vd + 128 * k, p_desc + (k >> 2) * 512 + 2 * (k & 3), idesc_v,
+                            (t > 0 || k > 0) ? 1u : 0u);
+            mma_commit_in(el, bar(kBarVEmpty + vslot));
+            if (++vslot == kPgVSlots) {
+              vslot = 0;
+              vphase ^= 1u;
+            }
+          }
+          if (m == 0 && more) {
+            // The rope half on top of the codes' sums.  Only products of one shape are ordered by their issue; these two
+            // differ in the depth of a step, so a barrier stands between them (a part of the value product fills it).
+            if (!(ok = warp_wait(bar(kBarCodes), uint32_t(n) & 1u))) break;
+            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t kd = smem_desc(sbase + kPgK + kslot * kPgSlot, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss_in(el, tmem, qr_desc + 2 * k, kd + 2 * k, idesc_r, 1u);
+            mma_commit_in(el, bar(kBarKEmpty + kslot));
+            mma_commit_in(el, bar(kBarSFull));
+            if (++kslot == kPgKSlots) {
+              kslot = 0;
+              kphase ^= 1u;
+            }
+            ++n;
+          }
+        }
+        if (ok && t >= 0) mma_commit_in(el, bar(kBarPFree));
       }
-      __syncwarp();
+      walk.advance(nt);
+      ++seg;
     }
+    // every product issued above must be complete before tensor memory is released
+    mma_commit_in(el, bar(kBarDrain));
+    mbar_drain(bar(kBarDrain), 0);
   } else if (warp < kPgSoft) {
-    reg_inc<kPgRegsV>();
-    // ---------------------------------------------------------------- queries and values
+    // ---------------------------------------------------------------- values
     const int vt = threadIdx.x - 32 * kPgVWarp;
-    const int vw = warp - kPgVWarp;
-    // Codes 16 g .. 16 g + 15 of rows r0 + 16 j: segments 2 (g % 4) and the next of
+    // Codes 16 g .. 16 g + 15 of rows r0 + 32 j: segments 2 (g % 4) and the next of
     // chunk g / 4 of the widened row.  Eight lanes take the first chunk of a row and
     // the second of its neighbour: with the swizzle, their stores fill all banks.
     const int g = vt & 7, r0 = (vt >> 3) ^ (g >> 2);
     const uint32_t voff = uint32_t((g >> 2) * kPgSlot + r0 * 128);
     const uint32_t seg0 = uint32_t(((2 * (g & 3)) ^ (r0 & 7)) << 4), seg1 = seg0 ^ 16u;
+    const uint8_t* base = c.kv8 + 16 * g;
     const int total = walk.left;
-    int slot = 0, seg = 0, row_tiles = 0;
+    int slot = 0;
     uint32_t sphase = 0;
     bool ok = true;
-    auto wait = [&](uint32_t b, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(b, parity, lim, abort_flag)) != 0;
-    };
-    // The codes of a slot are loaded two slots ahead, across tiles and rows.
-    const uint8_t* base = c.kv8 + 16 * g;
-    int y[8];
+    int y[4];
     auto rows = [&](int n) {
       const int rb = n % kPgRows;
-      if (!(ok = wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) return;
+      if (!(ok = group_wait(2, kPgVWarp, bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) return;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = row_s[rb * 128 + r0 + 16 * j];
+      for (int j = 0; j < 4; ++j) y[j] = reinterpret_cast<const int*>(keys_of(n))[r0 + 32 * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
     };
-    uint4 w0[8], w1[8];
-    auto widen = [&](const uint4 (&w)[8]) {  // into the next slot
-      if (!wait(bar(kBarVEmpty + slot), sphase ^ 1u)) return false;
+    auto widen = [&](const uint4 (&w)[4]) {  // into the next slot
+      if (!group_wait(2, kPgVWarp, bar(kBarVEmpty + slot), sphase ^ 1u)) return false;
       uint8_t* dst = smem + kPgV + slot * 2 * kPgSlot + voff;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) store_fp16(dst + j * 2048 + seg0, dst + j * 2048 + seg1, w[j]);
+      for (int j = 0; j < 4; ++j) store_fp16(dst + j * 4096 + seg0, dst + j * 4096 + seg1, w[j]);
       fence_proxy_async_smem();
-      mbar_arrive(bar(kBarVFull + slot));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarVFull + slot));
       if (++slot == kPgVSlots) {
         slot = 0;
         sphase ^= 1u;
       }
       return true;
     };
+    // The codes of a slot are loaded two slots ahead, across tiles and rows.
+    uint4 w0[4], w1[4];
     rows(0);
     if (ok) {
       load_codes(w0, y, base, 0);
       load_codes(w1, y, base, 128);
     }
-    for (int n = 0; n < total && ok; ++n) {
-      if (row_tiles == 0) {
-        // --- the query row: hi and lo codes and the scaled rope half
-        if (!(ok = wait(bar(kBarQEmpty), uint32_t(seg & 1) ^ 1u))) break;
-#pragma unroll 2
-        for (int i = 0; i < 16; ++i) {
-          const int h = vw * 16 + i;
-          const uint16_t* qh = q + ((long long)walk.t * 64 + h) * 576;
-          const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 16 * lane);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(qh + 16 * lane + 8);
-          const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
-          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          uint32_t amax = 0;
-          auto see = [&](uint32_t bits) {
-            bits &= 0x7fffffffu;
-            if (bits < 0x7f800000u) amax = max(amax, bits);
-          };
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            see(w[j] << 16);
-            see(w[j] & 0xffff0000u);
-          }
-          see(xr << 16);
-          see(xr & 0xffff0000u);
-          amax = __reduce_max_sync(0xffffffffu, amax);
-          // 2^e with max |q| <= 448 2^e
-          const int e0 = int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
-          const int e = max(e0, -100);
-          const float inv = pow2f(-e);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float v[4] = {__uint_as_float(w[2 * j] << 16), __uint_as_float(w[2 * j] & 0xffff0000u),
-                          __uint_as_float(w[2 * j + 1] << 16), __uint_as_float(w[2 * j + 1] & 0xffff0000u)};
-            uint32_t hh = 0, ll = 0;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              float a = v[2 * p] * inv, bb = v[2 * p + 1] * inv;
-              // an infinite value is taken as NaN (codes have no infinity): so is every score with it
-              if (isinf(a)) a = __uint_as_float(0x7fc00000u);
-              if (isinf(bb)) bb = __uint_as_float(0x7fc00000u);
-              const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(a, bb), __NV_SATFINITE, __NV_E4M3);
-              const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c2, __NV_E4M3)));
-              const __nv_fp8x2_storage_t d2 =
-                  __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (bb - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-              hh |= uint32_t(c2) << (16 * p);
-              ll |= uint32_t(d2) << (16 * p);
-            }
-            hi[j] = hh;
-            lo[j] = ll;
-          }
-          // lane holds codes 16 lane ..: chunk lane / 8, segment lane % 8
-          uint8_t* dst = smem + kPgQ8 + (lane >> 3) * kPgSlot + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + 64 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) =
-              __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
-          if (lane == 0) g_s[64 * (seg & 1) + h] = pow2f(e);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kBarQFull));
-        row_tiles = walk.segment();
-        walk.advance(row_tiles);
-        ++seg;
-      }
-      --row_tiles;
+#pragma unroll 1
+    for (int i = 0; i < 2 * total && ok; ++i) {  // half a tile
       if (!(ok = widen(w0))) break;
-      load_codes(w0, y, base, 256);
-      if (!(ok = widen(w1))) break;
-      load_codes(w1, y, base, 384);
-      if (!(ok = widen(w0))) break;
-      const bool more = n + 1 < total;
-      if (more) {
-        rows(n + 1);
+      if (i & 1) {
+        if (i + 1 < 2 * total) rows((i + 1) >> 1);
         if (!ok) break;
-        load_codes(w0, y, base, 0);
       }
+      const int col = (i & 1) ? 0 : 256;
+      const bool more = i + 1 < 2 * total;
+      if (more) load_codes(w0, y, base, col);
       if (!(ok = widen(w1))) break;
-      if (more) load_codes(w1, y, base, 128);
+      if (more) load_codes(w1, y, base, col + 128);
     }
   } else {
-    reg_inc<kPgRegsS>();
-    // ---------------------------------------------------------------- softmax
-    const int half = (warp - kPgSoft) >> 2;   // heads 32 half .. 32 half + 31
-    const int quarter = warp & 3;             // TMEM lanes of this warp
-    const int r = quarter * 32 + lane;        // its key of the tile, its dim of O^T
-    const int st = threadIdx.x - 32 * (kPgSoft + 4 * half);
-    const int bar_id = 1 + half;
+    // ---------------------------------------------------------------- softmax and queries
+    const int st = threadIdx.x - 32 * kPgSoft;
+    const int sw = warp - kPgSoft, quarter = warp & 3, w2 = sw >> 2;
     const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem + kPgRedOff) + half * 128;
-    const int h0 = 32 * half;
-    auto wait_all = [&](uint32_t b, uint32_t parity) {
-      const bool mine = st == 0 ? mbar_wait(b, parity, lim, abort_flag) : true;
-      return bar_red_or(bar_id, 128, mine ? 0 : 1) == 0;
-    };
+    const int part = lane >> 4;
+    const int head = 16 * quarter + (lane & 15);  // this thread's head, and its keys: key0 .. key0 + 31 of a tile
+    const int key0 = 64 * part + 32 * w2;
+    const int h0 = 32 * w2;                       // of O^T: lanes are dims, and this warp takes heads h0 .. h0 + 31
+    float* red = reinterpret_cast<float*>(smem + kPgRedOff);
     bool ok = true;
+
+    // The query of row `t` into tensor memory (codes) and shared memory (rope half).
+    auto query = [&](int t) {
+      const uint16_t* qt = q + (long long)t * 64 * 576;
+      // each head's largest value, a warp per head: 2^e with max |q| <= 448 2^e, and the rope half by it
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {
+        const int h = 8 * sw + i;
+        const uint16_t* qh = qt + h * 576;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 16 * lane);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(qh + 16 * lane + 8);
+        const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
+        const uint32_t w[9] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, xr};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          const uint32_t a = (w[j] << 16) & 0x7fffffffu, b = w[j] & 0x7fff0000u;
+          if (a < 0x7f800000u) amax = max(amax, a);
+          if (b < 0x7f800000u) amax = max(amax, b);
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const int e = max(int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+        const float inv = pow2f(-e);
+        const int row = 32 * (h >> 4) + (h & 15);
+        *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
+            __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
+        if (lane == 0) g_s[h] = pow2f(e);
+      }
+      named_bar_sync(1, 256);
+      // Codes: lane = row of the A operand.  The two lanes of a head split 16 dims, each makes hi and lo of its eight
+      // and they trade: the hi lane ends with 16 hi codes, the lo lane with 16 lo codes.
+      const float inv = 1.f / g_s[head];
+      const uint16_t* qh = qt + head * 576 + 256 * w2 + 8 * part;
+#pragma unroll 2
+      for (int i = 0; i < 16; i += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(qh + 16 * (i + k));
+        float f[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t hi[2], lo[2];
+          split_codes(v[k].x, v[k].y, inv, hi[0], lo[0]);
+          split_codes(v[k].z, v[k].w, inv, hi[1], lo[1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t mine = part ? lo[e] : hi[e];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, part ? hi[e] : lo[e], 16);
+            f[4 * k + e] = __uint_as_float(part ? got : mine);
+            f[4 * k + 2 + e] = __uint_as_float(part ? mine : got);
+          }
+        }
+        tmem_st16(lane_addr + kPgQCol + 64 * w2 + 4 * i, f);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQFull));
+    };
+
+    // the lo rows of the rope half stay zero
+    for (int i = st; i < 64 * 8; i += 256)
+      *reinterpret_cast<uint4*>(smem + kPgQR + (32 * (i >> 7) + 16 + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+    query(walk.t);
     int n = 0, seg = 0;
     int2 split = make_int2(-1, 0);
-    while (ok && walk.left > 0) {
+    while (ok && walk.left > 0) {  // (`ok` is the same in all threads of the role)
       const int nt = walk.segment();
-      f32x2 l_acc[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) l_acc[i] = 0ull;
-      if (st < 32) {
-        m_s[h0 + st] = -INFINITY;
-        off_s[h0 + st] = kPgNone;
-      }
-      for (int t = 0; t < nt && ok; ++t, ++n) {
-        // (the barrier in here also publishes m_s; the scores' barrier follows the query's, so 2^e is there too)
-        if (!(ok = wait_all(bar(kBarSFull + (n & 1)), uint32_t(n >> 1) & 1u))) break;
+      const float g = g_s[head];
+      const f32x2 g2 = f2_pack(g, g);
+      float m = -INFINITY, off = kPgNone;  // running maximum (a whole number) and kPgShift - m
+      f32x2 l2 = 0ull;
+      for (int t = 0; t < nt; ++t, ++n) {
+        // Of this head and 32 keys: x = y - m + kPgShift, y = S log2(e) + k (-inf where there is no key).  k and m are
+        // whole numbers, so x takes one rounding, of its own size.  Above kPgShift + kLazyRescale in some thread (pass
+        // 0): the heads' maxima of y (pass 1) give new m, and x is taken again (pass 2).
+        if (!(ok = group_wait(1, kPgSoft, bar(kBarSFull), uint32_t(n) & 1u))) break;
         tc_fence_after();
-        const int rb = n % kPgRows;
-        const bool valid = row_s[rb * 128 + r] >= 0;
-        const float sc = scale_s[rb * 128 + r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
-        // Of this key (-inf without one) and 32 heads: x = y - m + kPgShift, y = S log2(e) + k.  k and m are whole
-        // numbers, so x takes one rounding, of its own size.  Above kPgShift + kLazyRescale for some head of some key
-        // (pass 0): the maxima of y (pass 1) give new m, and x is taken again (pass 2).
-        const float cs = sc * scale_log2;
-        const float kf = valid ? float(int(__float_as_uint(sc) >> 23) - 127) : -INFINITY;
-        const f32x2 cs2 = f2_pack(cs, cs), kf2 = f2_pack(kf, kf), c16 = f2_pack(0.0625f, 0.0625f);
-        const uint32_t sa = lane_addr + 128 * (n & 1) + h0;
-        const ulonglong2* g4 = reinterpret_cast<const ulonglong2*>(g_s + 64 * (seg & 1) + h0);
-        const ulonglong2* off4 = reinterpret_cast<const ulonglong2*>(off_s + h0);
+        const float* cs_s = reinterpret_cast<const float*>(keys_of(n)) + 128 + key0;
         f32x2 x[16];
         int resc = 0;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
+          const float o = pass == 1 ? 0.f : off;
+          const f32x2 off2 = f2_pack(o, o), c16 = f2_pack(0.0625f, 0.0625f);
           float top = -INFINITY;
 #pragma unroll
           for (int i0 = 0; i0 < 16; i0 += 4) {
             float hi[8], lo[8];
-            tmem_ld8x2_sync(sa + 2 * i0, sa + 64 + 2 * i0, hi, lo);
+            tmem_ld_halves8x2_sync<64>(lane_addr + h0 + 2 * i0, lane_addr + (16u << 16) + h0 + 2 * i0, hi, lo);
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-              const ulonglong2 g = g4[(i0 + i) >> 1];
-              ulonglong2 off = off4[(i0 + i) >> 1];
-              if (pass == 1) off = make_ulonglong2(0ull, 0ull);
+              const ulonglong2 cs = *reinterpret_cast<const ulonglong2*>(cs_s + 2 * (i0 + i));
+              const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(cs_s + 128 + 2 * (i0 + i));
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int k = i + e;
                 const f32x2 d = f2_fma(f2_pack(lo[2 * k], lo[2 * k + 1]), c16, f2_pack(hi[2 * k], hi[2 * k + 1]));
-                x[i0 + k] = f2_fma(d, f2_mul(e ? g.y : g.x, cs2), f2_add(kf2, e ? off.y : off.x));
+                x[i0 + k] = f2_fma(d, f2_mul(e ? cs.y : cs.x, g2), f2_add(e ? kk.y : kk.x, off2));
                 float a0, a1;
                 f2_unpack(x[i0 + k], a0, a1);
                 top = fmaxf(top, fmaxf(a0, a1));
               }
             }
           }
-          if (pass == 0 && !bar_red_or(bar_id, 128, top > kPgShift + kLazyRescale ? 1 : 0)) break;
+          if (pass == 0 && !bar_red_or(1, 256, top > kPgShift + kLazyRescale)) break;
           if (pass == 1) {
-#pragma unroll
-            for (int i0 = 0; i0 < 16; i0 += 8) {
-              float v[16];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f2_unpack(x[i0 + i], v[2 * i], v[2 * i + 1]);
-              const float mx = reduce_scatter16<true>(v);
-              if (lane < 16) red[quarter * 32 + 2 * i0 + lane] = mx;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (part == 0) red[64 * w2 + head] = top;
+            named_bar_sync(1, 256);
+            const float mt = floorf(fmaxf(red[head], red[64 + head]));
+            float al = 1.f;
+            if (mt >= m + kLazyRescale && mt > m) {
+              al = m == -INFINITY ? 0.f : fast_exp2(m - mt);
+              m = mt;
+              off = kPgShift - mt;
             }
-            named_bar_sync(bar_id, 128);
-            int mine = 0;
-            if (st < 32) {
-              const float mt = floorf(fmaxf(fmaxf(red[st], red[32 + st]), fmaxf(red[64 + st], red[96 + st])));
-              const float mu = m_s[h0 + st];
-              float al = 1.f;
-              if (mt >= mu + kLazyRescale && mt > mu) {
-                al = mu == -INFINITY ? 0.f : fast_exp2(mu - mt);
-                m_s[h0 + st] = mt;
-                off_s[h0 + st] = kPgShift - mt;
-                mine = t > 0;
-              }
-              alpha_s[h0 + st] = al;
-            }
-            resc = bar_red_or(bar_id, 128, mine);  // also publishes m_s, off_s and alpha_s
+            l2 = f2_mul(l2, f2_pack(al, al));
+            if (sw < 4 && part == 0) alpha_s[head] = al;
+            resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSFree));
         // P and O are free once the previous value product is done
-        if (t > 0 && !(ok = wait_all(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
+        if (t > 0 && !(ok = group_wait(1, kPgSoft, bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
         if (resc) {
           tc_fence_after();
+          // O^T (lane = dim, column = head) *= alpha[head]
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            float o[32];
-            const uint32_t a = lane_addr + kPgOCol + 64 * m + h0;
-            tmem_ld32_sync(a, o);
+          for (int mm = 0; mm < 4; ++mm) {
+#pragma unroll 1
+            for (int hh = 0; hh < 32; hh += 16) {
+              float ov[16];
+              const uint32_t a = lane_addr + kPgOCol + 64 * mm + h0 + hh;
+              tmem_ld16_sync(a, ov);
 #pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] *= alpha_s[h0 + h];
-            tmem_st16(a, o);
-            tmem_st16(a + 16, o + 16);
+              for (int h = 0; h < 16; ++h) ov[h] *= alpha_s[h0 + hh + h];
+              tmem_st16(a, ov);
+            }
           }
           tmem_wait_st();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) l_acc[i] = f2_mul(l_acc[i], *reinterpret_cast<const f32x2*>(&alpha_s[h0 + 2 * i]));
         }
-        // u = 2^x, rounded to fp16 for the value product; the sums take it unrounded
-        const float inv = valid ? pow2f(127 - int(__float_as_uint(sc) >> 23)) : 0.f;
-        const f32x2 inv2 = f2_pack(inv, inv);
-        uint8_t* prow = smem + kPgP + r * 128;
+        // u = 2^x, rounded to fp16 for the value product; the sum takes it unrounded
+        uint8_t* prow = smem + kPgP + part * 8192 + head * 128;
 #pragma unroll
         for (int i0 = 0; i0 < 16; i0 += 4) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a0, a1;
-            f2_unpack(x[i0 + i], a0, a1);
-            a0 = fast_exp2(a0);
-            a1 = fast_exp2(a1);
-            l_acc[i0 + i] = f2_fma(f2_pack(a0, a1), inv2, l_acc[i0 + i]);
-            const __half2 p = __floats2half2_rn(a0, a1);
-            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+          for (int i = 0; i < 4; i += 2) {
+            const ulonglong2 inv = *reinterpret_cast<const ulonglong2*>(cs_s + 256 + 2 * (i0 + i));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float a0, a1;
+              f2_unpack(x[i0 + i + e], a0, a1);
+              a0 = fast_exp2(a0);
+              a1 = fast_exp2(a1);
+              l2 = f2_fma(f2_pack(a0, a1), e ? inv.y : inv.x, l2);
+              const __half2 p = __floats2half2_rn(a0, a1);
+              w[i + e] = *reinterpret_cast<const uint32_t*>(&p);
+            }
           }
-          *reinterpret_cast<uint4*>(prow + ((((h0 >> 3) + (i0 >> 2)) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(prow + (((4 * w2 + (i0 >> 2)) ^ (head & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(kBarPFull));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBarRowEmpty + n % kPgRows));
+          mbar_arrive(bar(kBarPFull));
+        }
       }
-      if (!ok) break;
-      // --- the row's (or the segment's) result
-      if (!(ok = wait_all(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int i0 = 0; i0 < 16; i0 += 8) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f2_unpack(l_acc[i0 + i], v[2 * i], v[2 * i + 1]);
-        const float l = reduce_scatter16<false>(v);
-        if (lane < 16) red[quarter * 32 + 2 * i0 + lane] = l;
-      }
-      named_bar_sync(bar_id, 128);
-      if (st < 32) l_s[h0 + st] = red[st] + red[32 + st] + red[64 + st] + red[96 + st];
-      named_bar_sync(bar_id, 128);
+      // --- the next row's query, then this row's (or this part's) result
+      const int row = walk.t, tile = walk.tile;
       const bool whole = nt == walk.ntiles;
+      if (!whole && tile == 0) {
+        const int rest = walk.ntiles - nt, share = start_s[4];
+        split = make_int2(row, 1 + (rest + share - 1) / share);
+      }
+      walk.advance(nt);
+      if (walk.left > 0) {
+        if (!ok || !(ok = group_wait(1, kPgSoft, bar(kBarQEmpty), uint32_t(seg & 1)))) break;
+        query(walk.t);
+      }
+      if (!ok || !(ok = group_wait(1, kPgSoft, bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
+      tc_fence_after();
+      float l, l1;
+      f2_unpack(l2, l, l1);
+      l += l1;
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (part == 0) red[64 * w2 + head] = l;
+      named_bar_sync(1, 256);
+      if (sw < 4 && part == 0) {
+        l = red[head] + red[64 + head];
+        l_s[head] = l;
+        m_s[head] = m;  // (l is 0 or NaN where there is no m)
+      }
+      named_bar_sync(1, 256);
       // a CTA leaves at most two partial results: of the row it starts inside (0) and of the row it ends inside (1)
-      float* prow = part + (long long)(2 * blockIdx.x + (walk.tile == 0 ? 1 : 0)) * kPartFloats;
+      float* prow = part_out + (long long)(2 * blockIdx.x + (tile == 0 ? 1 : 0)) * kPartFloats;
 #pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        float o[32];
-        tmem_ld32_sync(lane_addr + kPgOCol + 64 * m + h0, o);
-        const int d = 128 * m + r;
+      for (int mm = 0; mm < 4; ++mm) {
+        float ov[32];
+        tmem_ld32_sync(lane_addr + kPgOCol + 64 * mm + h0, ov);
+        const int d = 128 * mm + 32 * quarter + lane;
 #pragma unroll
         for (int h = 0; h < 32; ++h) {
           if (whole) {
-            const float l = l_s[h0 + h];
-            o_lat[((long long)walk.t * 64 + h0 + h) * 512 + d] = __float2bfloat16(l == 0.f ? 0.f : o[h] / l);
+            const float lh = l_s[h0 + h];
+            o_lat[((long long)row * 64 + h0 + h) * 512 + d] = __float2bfloat16(lh == 0.f ? 0.f : ov[h] / lh);
           } else {
-            prow[(h0 + h) * 512 + d] = o[h];
+            prow[(h0 + h) * 512 + d] = ov[h];
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(kBarOFree));
-      if (st < 32) {
-        const float l = l_s[h0 + st], m = m_s[h0 + st];  // (l is 0 or NaN where there is no m)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOFree));
+      if (st < 64) {
+        const float lh = l_s[st], mh = m_s[st];
         if (!whole) {
-          prow[64 * 512 + h0 + st] = m;
-          prow[64 * 512 + 64 + h0 + st] = l;
+          prow[64 * 512 + st] = mh;
+          prow[64 * 512 + 64 + st] = lh;
         } else if (lse) {
-          lse[(long long)walk.t * 64 + h0 + st] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
+          lse[(long long)row * 64 + st] = lh == 0.f ? -INFINITY : (mh - kPgShift + log2f(lh)) * 0.69314718055994531f;
         }
       }
-      if (!whole && walk.tile == 0) {
-        const int rest = walk.ntiles - nt, share = start_s[4];
-        split = make_int2(walk.t, 1 + (rest + share - 1) / share);
-      }
-      named_bar_sync(bar_id, 128);  // l_s, m_s are rewritten for the next row
-      walk.advance(nt);
       ++seg;
     }
-    if (half == 0 && st == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
+    if (st == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
   }
   pdl_trigger();
   tc_fence_before();
