@@ -14,9 +14,9 @@
 //
 // Values as fp16.  A code is exact in fp16, and a probability rounded to fp16
 // (2^-11) is eight times closer than one in bf16.  The row's 2^k goes into the
-// probability: with y = S log2(e) + k_s, u_s = 2^(y - m + 6) where m follows
-// the running maximum of y in whole numbers, so u is at most 2^14 (see kLazyRescale) and what
-// fp16 cannot hold is 2^-31 of the largest; sum u code is the numerator,
+// probability: with y = S log2(e) + k_s, u_s = 2^(y - m + 4) where m follows
+// the maximum of y in whole numbers, at most 11 behind: u is at most 2^15, and
+// what fp16 cannot hold is 2^-29 of the largest; sum u code is the numerator,
 // sum u 2^-k_s (fp32, u before rounding) the denominator.
 //
 // Shared memory carries no query: hi and lo lie in tensor memory as the A operand
@@ -31,8 +31,8 @@
 // after query row; a row that ends in another CTA leaves partial sums that
 // paged_mla_merge_kernel joins.  20 warps:
 //  * warp 3 finds each key's cache row and 2^k, up to four tiles ahead;
-//  * warps 0 and 1 copy the tile's rows (four chunks of 128 codes, then the rope
-//    chunk) into a ring of 16 KB slots, 128 bytes of 128 keys each, with cp.async;
+//  * warps 0 and 1 copy the tile's rows with cp.async, four chunks of 128 codes and
+//    the rope chunk, each 128 bytes of 128 keys;
 //  * warps 4..11 read the codes again (they are in L2 by then), widen them to
 //    fp16 and store them for the value product: two slots of 128 keys x 128 dims;
 //  * warps 12..19 are the softmax (a thread: one head, 32 keys) and prepare the
@@ -55,12 +55,13 @@ namespace {
 constexpr int kPgThreads = 640;       // five warps per scheduler: 96 registers a thread
 constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 12;  // first warp of each role (keys: 0)
 constexpr int kPgSlot = 16384;        // 128 keys x 128 bytes, 128B-swizzled
-constexpr int kPgKSlots = 7;
-constexpr int kPgVSlots = 2;
+constexpr int kPgKSlots = 5;          // the five chunks of a tile, each in a place of its own
+constexpr int kPgKGroups = 3;         // waited for together: codes 0..255, codes 256..511, rope
+constexpr int kPgVSlots = 2;          // dims 128 m .. 128 m + 127 go to slot m % 2
 constexpr int kPgRows = 4;            // tiles whose keys are described
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
-constexpr float kPgShift = 6.f;       // log2 of the probability at the running maximum
-constexpr float kPgNone = 1e30f;      // shift of a head without a maximum yet: any finite score sets one
+constexpr float kPgShift = 4.f;       // log2 of the probability at the running maximum ...
+constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much (fp16 ends at 2^16)
 
 constexpr int kPgQR = 0;                                     // the query's rope half: 128 rows (hi rows; lo rows are 0) x 64 bf16
 constexpr int kPgP = kPgQR + kPgSlot;                        // 2 chunks of 64 heads x 64 keys fp16
@@ -72,11 +73,11 @@ constexpr int kPgMOff = kPgRedOff + 512;                     // float m[64], alp
 constexpr int kPgBarOff = kPgMOff + 1024;
 enum PgBar {
   kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarSFull, kBarSFree, kBarDrain,
-  kBarKFull, kBarKEmpty = kBarKFull + kPgKSlots, kBarVFull = kBarKEmpty + kPgKSlots,
+  kBarKFull, kBarKEmpty = kBarKFull + kPgKGroups, kBarVFull = kBarKEmpty + kPgKGroups,
   kBarVEmpty = kBarVFull + kPgVSlots, kBarRowFull = kBarVEmpty + kPgVSlots, kBarRowEmpty = kBarRowFull + kPgRows,
   kPgBars = kBarRowEmpty + kPgRows
 };
-constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, abort flag, start (b, t, tile, tiles), share
+constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, then start (b, t, tile, tiles), share
 constexpr int kPgSmem = kPgTailOff + 64;
 constexpr int kPgSmemAlloc = kPgSmem + 1024;
 constexpr uint32_t kPgQCol = 128, kPgOCol = 256;             // S: 128 columns; Q: 128 (512 codes); O^T: 4 x 64
@@ -151,11 +152,14 @@ __device__ __forceinline__ long long tiles_of(int nq, long long len, int topk_ti
   return none + tiles_below(max(0ll, base + j)) - tiles_below(max(0ll, base));
 }
 
-// Codes 16 g .. 16 g + 15 (+ col) of a thread's four keys; zeros where there is no key.
-__device__ __forceinline__ void load_codes(uint4 (&w)[4], const int (&y)[4], const uint8_t* base, int col) {
+// Sixteen codes of each of a thread's four keys; zeros where the tile has no key at all.
+__device__ __forceinline__ void load_codes(uint4 (&w)[4], const uint8_t* const (&src)[4], int col, bool any) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = y[j] >= 0 ? *reinterpret_cast<const uint4*>(base + (long long)y[j] * kRow8 + col) : make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < 4; ++j) w[j] = make_uint4(0, 0, 0, 0);
+  if (any) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(src[j] + col);
+  }
 }
 
 // Sixteen codes as fp16, into two 16-byte segments.
@@ -207,9 +211,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   float* l_s = m_s + 128;
   float* g_s = m_s + 192;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kPgTailOff + 4);
   int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile, tiles of this CTA, tiles of a share
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (by a shuffle, so that the compiler knows it to be the same in all lanes: the roles' addresses and descriptors
+  // then live in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int topk_tiles = kSparse ? (topk + 127) >> 7 : 0;
 
   if (threadIdx.x == 0) {
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     mbar_init(bar(kBarSFull), 1);
     mbar_init(bar(kBarSFree), 8);
     mbar_init(bar(kBarDrain), 1);
-    for (int i = 0; i < kPgKSlots; ++i) {
+    for (int i = 0; i < kPgKGroups; ++i) {
       mbar_init(bar(kBarKFull + i), 64);  // every copying thread
       mbar_init(bar(kBarKEmpty + i), 1);
     }
@@ -234,7 +239,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(bar(kBarRowFull + i), 1);
       mbar_init(bar(kBarRowEmpty + i), 18);  // the key, value and softmax warps
     }
-    *abort_flag = 0;
     start_s[3] = 0;
     fence_mbar_init();
   }
@@ -299,28 +303,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at 0
   TileWalk walk{c, cu_q, seq_len, T, topk_tiles, 0, 0, 0, 0, 0, 0, 0};
   const bool busy = start_s[3] > 0;
   if (busy) walk.start(start_s);
   else if (threadIdx.x == 0) meta[blockIdx.x] = make_int2(-1, 0);
 
-  // A bounded wait of a whole warp, short in code (see the rolled loops of the
-  // issuing warp); the lanes agree on its outcome.
+  // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back in some 10 ns, so the
+  // limit is counted in tries: the code of 18 waits has to stay short (see the issuing warp).  Who gives up leaves its
+  // loop; the roles that wait for it run into their own limits.
+  const uint32_t tries = uint32_t(min(lim.ns / 10, 2000000000ull)) + 1;
   auto warp_wait = [&](uint32_t b, uint32_t parity) {
-    bool done = mbar_try_wait(b, parity);
-    if (!done) {
-      const unsigned long long t0 = globaltimer();
+    uint32_t left = tries;
+    bool done;
 #pragma unroll 1
-      do {
-        done = mbar_try_wait(b, parity);
-      } while (!done && !*abort_flag && globaltimer() - t0 <= lim.ns);
-    }
-    done = __all_sync(0xffffffffu, done);
-    if (!done) {
-      if (lane == 0 && !*abort_flag) raise_status(kStatusTimeout);
-      *abort_flag = 1;
-    }
+    do done = __all_sync(0xffffffffu, mbar_try_wait(b, parity)) != 0;
+    while (!done && --left);
     return done;
   };
   // The same for a role of 256 threads: one warp tries, the others stand at a
@@ -335,32 +333,30 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   } else if (warp < kPgMma) {
     // ---------------------------------------------------------------- keys
     const int g = threadIdx.x & 7, r0 = threadIdx.x >> 3;  // segment g of rows r0 + 8 j
-    const uint32_t off = uint32_t(r0 * 128 + ((g ^ r0) << 4));
+    const uint32_t dst = sbase + kPgK + uint32_t(r0 * 128 + ((g ^ r0) << 4));
     const uint8_t* base = c.kv8 + 16 * g;
-    int slot = 0;
-    uint32_t sphase = 0;
     bool ok = true;
     for (int n = 0; n < walk.left && ok; ++n) {
       const int rb = n % kPgRows;
       if (!(ok = warp_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) break;
-      int y[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] = reinterpret_cast<const int*>(keys_of(n))[r0 + 8 * j];
+      const int* row_s = reinterpret_cast<const int*>(keys_of(n)) + r0;
+      const bool none = row_s[0] < 0;
+#pragma unroll 1
+      for (int gr = 0; gr < kPgKGroups; ++gr) {
+        if (!(ok = warp_wait(bar(kBarKEmpty + gr), (uint32_t(n) & 1u) ^ 1u))) break;
+#pragma unroll 4
+        for (int j = 0; j < 16; ++j) {
+          const uint8_t* src = base + (long long)max(row_s[8 * j], 0) * kRow8 + 256 * gr;
+          const uint32_t d = dst + 2 * gr * kPgSlot + j * 1024;
+          cp_async_16_or_zero(d, src, none);
+          if (gr < 2) cp_async_16_or_zero(d + kPgSlot, src + 128, none);
+        }
+        cp_async_arrive_noinc(bar(kBarKFull + gr));
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
-      for (int ch = 0; ch < 5; ++ch) {
-        if (!(ok = warp_wait(bar(kBarKEmpty + slot), sphase ^ 1u))) break;
-        const uint32_t dst = sbase + kPgK + slot * kPgSlot + off;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          cp_async_16_or_zero(dst + j * 1024, base + (long long)max(y[j], 0) * kRow8 + 128 * ch, y[j] < 0);
-        cp_async_arrive_noinc(bar(kBarKFull + slot));
-        if (++slot == kPgKSlots) {
-          slot = 0;
-          sphase ^= 1u;
-        }
-      }
     }
+    if (!ok && lane == 0) raise_status(kStatusTimeout);
     cp_async_wait_all();
   } else if (warp == kPgAddr) {
     // ---------------------------------------------------------------- addresses
@@ -424,14 +420,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     position();
     for (int n = 0; n < total; ++n) {
       const int rb = n % kPgRows;
-      if (!warp_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u)) break;
+      if (!warp_wait(bar(kBarRowEmpty + rb), (uint32_t(n / kPgRows) & 1u) ^ 1u)) {
+        if (lane == 0) raise_status(kStatusTimeout);
+        break;
+      }
       int* row_s = reinterpret_cast<int*>(keys_of(n)) + lane;
       float* cs_s = reinterpret_cast<float*>(row_s) + 128;
+      // A place without a key takes the row of one that has: it is read with weight 0, and what other rows of the cache
+      // hold (NaN perhaps) is not read.  -1 throughout where the tile has no key.
+      const int some = __reduce_max_sync(0xffffffffu, max(max(row0[0], row0[1]), max(row0[2], row0[3])));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = int(__float_as_uint(sc0[i]) >> 23);  // k + 127
         const bool has = row0[i] >= 0;
-        row_s[32 * i] = row0[i];
+        row_s[32 * i] = has ? row0[i] : some;
         cs_s[32 * i] = sc0[i] * scale_log2;
         cs_s[128 + 32 * i] = has ? float(e - 127) : -INFINITY;
         cs_s[256 + 32 * i] = has ? pow2f(127 - e) : 0.f;
@@ -449,35 +451,45 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint32_t idesc_r = idesc_bf16(128, 128, 0, 0);
     const uint32_t idesc_v = idesc_f16(128, 64, 1, 0);
     const uint64_t qr_desc = smem_desc(sbase + kPgQR, 16, 1024, kSwizzle128B);
+    const uint64_t k_desc = smem_desc(sbase + kPgK, 16, 1024, kSwizzle128B);
     const uint64_t p_desc = smem_desc(sbase + kPgP, 16, 1024, kSwizzle128B);
-    int kslot = 0, vslot = 0, n = 0, seg = 0;  // n: tiles whose scores are issued
-    uint32_t kphase = 0, vphase = 0;
+    const uint64_t v_desc = smem_desc(sbase + kPgV, kPgSlot, 1024, kSwizzle128B);
+    int n = 0, seg = 0;  // tiles whose scores are issued, rows begun
     bool ok = true;
-    // (the loops below stay rolled: five warps of four roles share a scheduler's instruction cache)
+    // Places and phases are fixed by the chunk (two uses of a value slot a tile: the phase is m / 2), so every
+    // descriptor is a constant: a product then costs this warp an instruction or two, and it is its instructions,
+    // one in some ten cycles beside the other roles, that bound the tile otherwise.
+    auto values = [&](int m, uint32_t add) {  // 128 dims of the value product
+      if (!warp_wait(bar(kBarVFull + (m & 1)), m >> 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mma_f16_ss_in(el, tmem + kPgOCol + 64 * m, v_desc + (m & 1) * (2 * kPgSlot >> 4) + 128 * k,
+                      p_desc + (k >> 2) * 512 + 2 * (k & 3), idesc_v, k ? 1u : add);
+      mma_commit_in(el, bar(kBarVEmpty + (m & 1)));
+      return true;
+    };
     while (ok && walk.left > 0) {
       const int nt = walk.segment();
       if (!(ok = warp_wait(bar(kBarQFull), uint32_t(seg & 1)))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int t = -1; t < nt && ok; ++t) {  // scores of tile t + 1, values of tile t
+      for (int t = -1; t < nt; ++t) {  // scores of tile t + 1, values of tile t
         const bool more = t + 1 < nt;
+        const uint32_t np = uint32_t(n) & 1u;
         if (more) {
           // S of the codes; the buffer is free once the softmax has read the tile before
-          if (n > 0 && !(ok = warp_wait(bar(kBarSFree), uint32_t(n - 1) & 1u))) break;
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) break;
+          if (n > 0 && !(ok = warp_wait(bar(kBarSFree), np ^ 1u))) break;
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr) {
+            if (!(ok = warp_wait(bar(kBarKFull + gr), np))) break;
             fence_proxy_async_smem();
             tc_fence_after();
-            const uint64_t kd = smem_desc(sbase + kPgK + kslot * kPgSlot, 16, 1024, kSwizzle128B);
-            const uint32_t qa = tmem + kPgQCol + 32 * ch;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8_ts_in(el, tmem, qa + 8 * k, kd + 2 * k, idesc_k, (ch | k) ? 1u : 0u);
-            mma_commit_in(el, bar(kBarKEmpty + kslot));
-            if (++kslot == kPgKSlots) {
-              kslot = 0;
-              kphase ^= 1u;
-            }
+            for (int k = 8 * gr; k < 8 * gr + 8; ++k)
+              mma_f8_ts_in(el, tmem, tmem + kPgQCol + 8 * k, k_desc + (k >> 2) * (kPgSlot >> 4) + 2 * (k & 3), idesc_k,
+                           k ? 1u : 0u);
+            mma_commit_in(el, bar(kBarKEmpty + gr));
           }
           if (!ok) break;
           mma_commit_in(el, bar(kBarCodes));
@@ -485,51 +497,35 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           mma_commit_in(el, bar(kBarQEmpty));
         }
         if (t >= 0) {
-          if (!(ok = warp_wait(bar(kBarPFull), uint32_t(n - 1) & 1u))) break;
+          if (!(ok = warp_wait(bar(kBarPFull), np ^ 1u))) break;
           if (t == 0 && seg > 0 && !(ok = warp_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u))) break;
+          if (!(ok = values(0, t > 0 ? 1u : 0u))) break;
+        }
+        if (more) {
+          // The rope half on top of the codes' sums.  Only products of one shape are ordered by their issue; these two
+          // differ in the depth of a step, so a barrier stands between them (a part of the value product fills it).
+          if (!(ok = warp_wait(bar(kBarCodes), np))) break;
+          if (!(ok = warp_wait(bar(kBarKFull + 2), np))) break;
+          fence_proxy_async_smem();
           tc_fence_after();
-        }
-#pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          if (t >= 0) {  // 128 dims of the value product
-            if (!(ok = warp_wait(bar(kBarVFull + vslot), vphase))) break;
-            tc_fence_after();
-            const uint64_t vd = smem_desc(sbase + kPgV + vslot * 2 * kPgSlot, kPgSlot, 1024, kSwizzle128B);
-            const uint32_t od = tmem + kPgOCol + 64 * m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ss_in(el, od, vd + 128 * k, p_desc + (k >> 2) * 512 + 2 * (k & 3), idesc_v,
-                            (t > 0 || k > 0) ? 1u : 0u);
-            mma_commit_in(el, bar(kBarVEmpty + vslot));
-            if (++vslot == kPgVSlots) {
-              vslot = 0;
-              vphase ^= 1u;
-            }
-          }
-          if (m == 0 && more) {
-            // The rope half on top of the codes' sums.  Only products of one shape are ordered by their issue; these two
-            // differ in the depth of a step, so a barrier stands between them (a part of the value product fills it).
-            if (!(ok = warp_wait(bar(kBarCodes), uint32_t(n) & 1u))) break;
-            if (!(ok = warp_wait(bar(kBarKFull + kslot), kphase))) break;
-            fence_proxy_async_smem();
-            tc_fence_after();
-            const uint64_t kd = smem_desc(sbase + kPgK + kslot * kPgSlot, 16, 1024, kSwizzle128B);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss_in(el, tmem, qr_desc + 2 * k, kd + 2 * k, idesc_r, 1u);
-            mma_commit_in(el, bar(kBarKEmpty + kslot));
-            mma_commit_in(el, bar(kBarSFull));
-            if (++kslot == kPgKSlots) {
-              kslot = 0;
-              kphase ^= 1u;
-            }
-            ++n;
-          }
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ss_in(el, tmem, qr_desc + 2 * k, k_desc + 4 * (kPgSlot >> 4) + 2 * k, idesc_r, 1u);
+          mma_commit_in(el, bar(kBarKEmpty + 2));
+          mma_commit_in(el, bar(kBarSFull));
+          ++n;
         }
-        if (ok && t >= 0) mma_commit_in(el, bar(kBarPFree));
+        if (t >= 0) {
+          if (!(ok = values(1, t > 0 ? 1u : 0u)) || !(ok = values(2, t > 0 ? 1u : 0u)) ||
+              !(ok = values(3, t > 0 ? 1u : 0u)))
+            break;
+          mma_commit_in(el, bar(kBarPFree));
+        }
       }
       walk.advance(nt);
       ++seg;
     }
+    if (!ok && lane == 0) raise_status(kStatusTimeout);
     // every product issued above must be complete before tensor memory is released
     mma_commit_in(el, bar(kBarDrain));
     mbar_drain(bar(kBarDrain), 0);
@@ -543,53 +539,51 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint32_t voff = uint32_t((g >> 2) * kPgSlot + r0 * 128);
     const uint32_t seg0 = uint32_t(((2 * (g & 3)) ^ (r0 & 7)) << 4), seg1 = seg0 ^ 16u;
     const uint8_t* base = c.kv8 + 16 * g;
+    uint8_t* const dst = smem + kPgV + voff;
     const int total = walk.left;
-    int slot = 0;
-    uint32_t sphase = 0;
-    bool ok = true;
-    int y[4];
+    bool ok = true, any = false;
+    const uint8_t* src[4];
     auto rows = [&](int n) {
       const int rb = n % kPgRows;
-      if (!(ok = group_wait(2, kPgVWarp, bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) return;
+      if (!group_wait(2, kPgVWarp, bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u)) return false;
+      const int* row_s = reinterpret_cast<const int*>(keys_of(n)) + r0;
+      any = row_s[0] >= 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = reinterpret_cast<const int*>(keys_of(n))[r0 + 32 * j];
+      for (int j = 0; j < 4; ++j) src[j] = base + (long long)max(row_s[32 * j], 0) * kRow8;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+      return true;
     };
-    auto widen = [&](const uint4 (&w)[4]) {  // into the next slot
-      if (!group_wait(2, kPgVWarp, bar(kBarVEmpty + slot), sphase ^ 1u)) return false;
-      uint8_t* dst = smem + kPgV + slot * 2 * kPgSlot + voff;
+    auto widen = [&](const uint4 (&w)[4], int sl, uint32_t parity) {  // into slot `sl`
+      if (!group_wait(2, kPgVWarp, bar(kBarVEmpty + sl), parity)) return false;
+      uint8_t* d = dst + sl * 2 * kPgSlot;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) store_fp16(dst + j * 4096 + seg0, dst + j * 4096 + seg1, w[j]);
+      for (int j = 0; j < 4; ++j) store_fp16(d + j * 4096 + seg0, d + j * 4096 + seg1, w[j]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarVFull + slot));
-      if (++slot == kPgVSlots) {
-        slot = 0;
-        sphase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive(bar(kBarVFull + sl));
       return true;
     };
     // The codes of a slot are loaded two slots ahead, across tiles and rows.
     uint4 w0[4], w1[4];
-    rows(0);
-    if (ok) {
-      load_codes(w0, y, base, 0);
-      load_codes(w1, y, base, 128);
+    if ((ok = rows(0))) {
+      load_codes(w0, src, 0, any);
+      load_codes(w1, src, 128, any);
     }
 #pragma unroll 1
-    for (int i = 0; i < 2 * total && ok; ++i) {  // half a tile
-      if (!(ok = widen(w0))) break;
-      if (i & 1) {
-        if (i + 1 < 2 * total) rows((i + 1) >> 1);
-        if (!ok) break;
-      }
-      const int col = (i & 1) ? 0 : 256;
+    for (int i = 0; i < 2 * total && ok; ++i) {  // half a tile: 256 dims
+      const uint32_t parity = uint32_t(i & 1) ^ 1u;
+      if (!(ok = widen(w0, 0, parity))) break;
       const bool more = i + 1 < 2 * total;
-      if (more) load_codes(w0, y, base, col);
-      if (!(ok = widen(w1))) break;
-      if (more) load_codes(w1, y, base, col + 128);
+      const int col = (i & 1) ? 0 : 256;
+      if (more) {
+        if ((i & 1) && !(ok = rows((i + 1) >> 1))) break;
+        load_codes(w0, src, col, any);
+      }
+      if (!(ok = widen(w1, 1, parity))) break;
+      if (more) load_codes(w1, src, col + 128, any);
     }
+    if (!ok && vt == 0) raise_status(kStatusTimeout);
   } else {
     // ---------------------------------------------------------------- softmax and queries
     const int st = threadIdx.x - 32 * kPgSoft;
@@ -673,70 +667,77 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       const int nt = walk.segment();
       const float g = g_s[head];
       const f32x2 g2 = f2_pack(g, g);
-      float m = -INFINITY, off = kPgNone;  // running maximum (a whole number) and kPgShift - m
+      // the head's running maximum m of y (a whole number), off = kPgShift - m, and the x that asks for a new one
+      float m = -INFINITY, off = 0.f, most = -INFINITY;
       f32x2 l2 = 0ull;
       for (int t = 0; t < nt; ++t, ++n) {
-        // Of this head and 32 keys: x = y - m + kPgShift, y = S log2(e) + k (-inf where there is no key).  k and m are
-        // whole numbers, so x takes one rounding, of its own size.  Above kPgShift + kLazyRescale in some thread (pass
-        // 0): the heads' maxima of y (pass 1) give new m, and x is taken again (pass 2).
+        // Of this head and 32 keys: x = y + off = y - m + kPgShift, y = S log2(e) + k (-inf where there is no key).  k and
+        // m are whole numbers, so x takes one rounding, of its own size (before there is an m, off is -k of the tile's
+        // first key).  Some x above kPgShift + kPgLazy, or a first maximum: the heads' maxima give a new m.
         if (!(ok = group_wait(1, kPgSoft, bar(kBarSFull), uint32_t(n) & 1u))) break;
         tc_fence_after();
         const float* cs_s = reinterpret_cast<const float*>(keys_of(n)) + 128 + key0;
+        if (m == -INFINITY) {
+          const float k0 = reinterpret_cast<const float*>(keys_of(n))[256];
+          off = k0 > -INFINITY ? -k0 : 0.f;
+        }
+        const f32x2 off2 = f2_pack(off, off), c16 = f2_pack(0.0625f, 0.0625f);
         f32x2 x[16];
-        int resc = 0;
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-          const float o = pass == 1 ? 0.f : off;
-          const f32x2 off2 = f2_pack(o, o), c16 = f2_pack(0.0625f, 0.0625f);
-          float top = -INFINITY;
+        float top = -INFINITY;
 #pragma unroll
-          for (int i0 = 0; i0 < 16; i0 += 4) {
-            float hi[8], lo[8];
-            tmem_ld_halves8x2_sync<64>(lane_addr + h0 + 2 * i0, lane_addr + (16u << 16) + h0 + 2 * i0, hi, lo);
+        for (int i0 = 0; i0 < 16; i0 += 4) {
+          float hi[8], lo[8];
+          tmem_ld_halves8x2_sync<64>(lane_addr + h0 + 2 * i0, lane_addr + (16u << 16) + h0 + 2 * i0, hi, lo);
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const ulonglong2 cs = *reinterpret_cast<const ulonglong2*>(cs_s + 2 * (i0 + i));
-              const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(cs_s + 128 + 2 * (i0 + i));
+          for (int i = 0; i < 4; i += 2) {
+            const ulonglong2 cs = *reinterpret_cast<const ulonglong2*>(cs_s + 2 * (i0 + i));
+            const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(cs_s + 128 + 2 * (i0 + i));
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int k = i + e;
-                const f32x2 d = f2_fma(f2_pack(lo[2 * k], lo[2 * k + 1]), c16, f2_pack(hi[2 * k], hi[2 * k + 1]));
-                x[i0 + k] = f2_fma(d, f2_mul(e ? cs.y : cs.x, g2), f2_add(e ? kk.y : kk.x, off2));
-                float a0, a1;
-                f2_unpack(x[i0 + k], a0, a1);
-                top = fmaxf(top, fmaxf(a0, a1));
-              }
+            for (int e = 0; e < 2; ++e) {
+              const int k = i + e;
+              const f32x2 d = f2_fma(f2_pack(lo[2 * k], lo[2 * k + 1]), c16, f2_pack(hi[2 * k], hi[2 * k + 1]));
+              x[i0 + k] = f2_fma(d, f2_mul(e ? cs.y : cs.x, g2), f2_add(e ? kk.y : kk.x, off2));
+              float a0, a1;
+              f2_unpack(x[i0 + k], a0, a1);
+              top = fmaxf(top, fmaxf(a0, a1));
             }
-          }
-          if (pass == 0 && !bar_red_or(1, 256, top > kPgShift + kLazyRescale)) break;
-          if (pass == 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            if (part == 0) red[64 * w2 + head] = top;
-            named_bar_sync(1, 256);
-            const float mt = floorf(fmaxf(red[head], red[64 + head]));
-            float al = 1.f;
-            if (mt >= m + kLazyRescale && mt > m) {
-              al = m == -INFINITY ? 0.f : fast_exp2(m - mt);
-              m = mt;
-              off = kPgShift - mt;
-            }
-            l2 = f2_mul(l2, f2_pack(al, al));
-            if (sw < 4 && part == 0) alpha_s[head] = al;
-            resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarSFree));
+        int resc = 0;
+        if (bar_red_or(1, 256, top > most)) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          if (part == 0) red[64 * w2 + head] = top;
+          named_bar_sync(1, 256);
+          const float mt = floorf(fmaxf(red[head], red[64 + head]) - off);
+          float al = 1.f;
+          if (mt > m && (m == -INFINITY || mt >= m + kPgLazy)) {
+            al = m == -INFINITY ? 0.f : fast_exp2(m - mt);
+            const float d = kPgShift - mt - off;
+            const f32x2 d2 = f2_pack(d, d);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = f2_add(x[i], d2);
+            m = mt;
+            off = kPgShift - mt;
+            most = kPgShift + kPgLazy;
+          }
+          l2 = f2_mul(l2, f2_pack(al, al));
+          if (sw < 4 && part == 0) alpha_s[head] = al;
+          resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
+        }
         // P and O are free once the previous value product is done
         if (t > 0 && !(ok = group_wait(1, kPgSoft, bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
         if (resc) {
           tc_fence_after();
-          // O^T (lane = dim, column = head) *= alpha[head]
+          // O^T (lane = dim, column = head) *= alpha[head], where a head of these 16 asks for it
+          const uint32_t ask = __ballot_sync(0xffffffffu, alpha_s[h0 + lane] != 1.f);
 #pragma unroll 1
-          for (int mm = 0; mm < 4; ++mm) {
+          for (int hh = 0; hh < 32; hh += 16) {
+            if (!((ask >> hh) & 0xffffu)) continue;
 #pragma unroll 1
-            for (int hh = 0; hh < 32; hh += 16) {
+            for (int mm = 0; mm < 4; ++mm) {
               float ov[16];
               const uint32_t a = lane_addr + kPgOCol + 64 * mm + h0 + hh;
               tmem_ld16_sync(a, ov);
@@ -833,7 +834,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       ++seg;
     }
-    if (st == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
+    if (st == 0) {
+      if (!ok) raise_status(kStatusTimeout);
+      meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
+    }
   }
   pdl_trigger();
   tc_fence_before();
@@ -841,7 +845,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   tc_fence_after();
   if (warp == kPgMma) {
     __syncwarp();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_slot, 512);
   }
 }
 

@@ -98,8 +98,8 @@ class Batch:
         and itself.  Probabilities are rounded to fp16, 2^-11, and sums in 32 bits again, 2^-17; the output to bf16,
         2^-8 of itself.  A relative error e of every weight moves a mean by at most 2 e times the mean magnitude.
         fp16 has a floor besides its relative step: what is rounded is u = p 2^k, held so that the largest u of a head
-        is at least 2^6 (the running maximum stands at 2^6 and is never above a score already seen); values below 2^-14
-        are rounded to multiples of 2^-24, so each u is off by up to 2^-25 more, 2^-31 of the largest, times its code.
+        is at least 2^4 (the running maximum stands at 2^4 and is never above a score already seen); values below 2^-14
+        are rounded to multiples of 2^-24, so each u is off by up to 2^-25 more, 2^-29 of the largest, times its code.
         """
         import torch
         o = torch.zeros(self.T, HEADS, LATENT, dtype=torch.float64, device="cuda")
@@ -129,7 +129,7 @@ class Batch:
                              + 2.0 ** -22 * q.abs().amax(1, keepdim=True) * k.abs().sum(1)[None]).amax(1) + 2.0 ** -20
                 tl[t] = e + 2.0 ** -22 * lse[t].abs()
                 to[t] = 2.0 ** -8 * o[t].abs() + (2 * e[:, None] + 2.0 ** -11 + 2.0 ** -16) * (p @ v.abs())
-                to[t] += 2.0 ** -31 * (p * ks).amax(1)[:, None] * (v.abs() / ks[:, None]).sum(0)[None]
+                to[t] += 2.0 ** -29 * (p * ks).amax(1)[:, None] * (v.abs() / ks[:, None]).sum(0)[None]
         return o, lse, to, tl
 
 
