@@ -57,7 +57,7 @@ constexpr int kPgMma = 2, kPgAddr = 3, kPgVWarp = 4, kPgSoft = 12;  // first war
 constexpr int kPgSlot = 16384;        // 128 keys x 128 bytes, 128B-swizzled
 constexpr int kPgKSlots = 5;          // the five chunks of a tile, each in a place of its own
 constexpr int kPgKGroups = 3;         // waited for together: codes 0..255, codes 256..511, rope
-constexpr int kPgVSlots = 2;          // dims 128 m .. 128 m + 127 go to slot m % 2
+constexpr int kPgVSlots = 3;          // of 128 dims: one product runs, one is ready, one is being widened
 constexpr int kPgRows = 4;            // tiles whose keys are described
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
 constexpr float kPgShift = 4.f;       // log2 of the probability at the running maximum ...
@@ -321,12 +321,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     while (!done && --left);
     return done;
   };
-  // The same for a role of 256 threads: one warp tries, the others stand at a
-  // barrier, where they take no issue slots (a try that fails comes back in some
-  // 20 cycles).  The barrier hands everyone the outcome.
-  auto group_wait = [&](int id, int leader, uint32_t b, uint32_t parity) {
-    const bool done = warp == leader ? warp_wait(b, parity) : true;
-    return bar_red_or(id, 256, done ? 0 : 1) == 0;
+  // The same for the softmax: one warp tries, and a barrier hands all 256 threads the outcome, so that they leave
+  // together if they have to.
+  auto group_wait = [&](uint32_t b, uint32_t parity) {
+    const bool done = warp == kPgSoft ? warp_wait(b, parity) : true;
+    return bar_red_or(1, 256, done ? 0 : 1) == 0;
   };
   if (!busy) {
     // nothing to do
@@ -341,20 +340,21 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (!(ok = warp_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u))) break;
       const int* row_s = reinterpret_cast<const int*>(keys_of(n)) + r0;
       const bool none = row_s[0] < 0;
-#pragma unroll 1
-      for (int gr = 0; gr < kPgKGroups; ++gr) {
-        if (!(ok = warp_wait(bar(kBarKEmpty + gr), (uint32_t(n) & 1u) ^ 1u))) break;
-#pragma unroll 4
-        for (int j = 0; j < 16; ++j) {
-          const uint8_t* src = base + (long long)max(row_s[8 * j], 0) * kRow8 + 256 * gr;
-          const uint32_t d = dst + 2 * gr * kPgSlot + j * 1024;
-          cp_async_16_or_zero(d, src, none);
-          if (gr < 2) cp_async_16_or_zero(d + kPgSlot, src + 128, none);
-        }
-        cp_async_arrive_noinc(bar(kBarKFull + gr));
-      }
+      const uint8_t* src[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) src[j] = base + (long long)max(row_s[8 * j], 0) * kRow8;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
+#pragma unroll
+      for (int gr = 0; gr < kPgKGroups; ++gr) {
+        if (!(ok = warp_wait(bar(kBarKEmpty + gr), (uint32_t(n) & 1u) ^ 1u))) break;
+#pragma unroll
+        for (int ch = 2 * gr; ch < min(2 * gr + 2, kPgKSlots); ++ch)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            cp_async_16_or_zero(dst + ch * kPgSlot + j * 1024, src[j] + 128 * ch, none);
+        cp_async_arrive_noinc(bar(kBarKFull + gr));
+      }
     }
     if (!ok && lane == 0) raise_status(kStatusTimeout);
     cp_async_wait_all();
@@ -456,21 +456,28 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint64_t v_desc = smem_desc(sbase + kPgV, kPgSlot, 1024, kSwizzle128B);
     int n = 0, seg = 0;  // tiles whose scores are issued, rows begun
     bool ok = true;
-    // Places and phases are fixed by the chunk (two uses of a value slot a tile: the phase is m / 2), so every
-    // descriptor is a constant: a product then costs this warp an instruction or two, and it is its instructions,
-    // one in some ten cycles beside the other roles, that bound the tile otherwise.
+    // The keys' places are fixed by the chunk, and all that addresses are made of is the same in all lanes, so descriptors
+    // stay in uniform registers: it is this warp's instructions, one in some ten cycles beside the other roles, that
+    // bound the tile otherwise.
+    int vs = 0;
+    uint32_t vp = 0;
     auto values = [&](int m, uint32_t add) {  // 128 dims of the value product
-      if (!warp_wait(bar(kBarVFull + (m & 1)), m >> 1)) return false;
+      if (!warp_wait(bar(kBarVFull + vs), vp)) return false;
       tc_fence_after();
+      const uint64_t vd = v_desc + vs * (2 * kPgSlot >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        mma_f16_ss_in(el, tmem + kPgOCol + 64 * m, v_desc + (m & 1) * (2 * kPgSlot >> 4) + 128 * k,
-                      p_desc + (k >> 2) * 512 + 2 * (k & 3), idesc_v, k ? 1u : add);
-      mma_commit_in(el, bar(kBarVEmpty + (m & 1)));
+        mma_f16_ss_in(el, tmem + kPgOCol + 64 * m, vd + 128 * k, p_desc + (k >> 2) * 512 + 2 * (k & 3), idesc_v,
+                      k ? 1u : add);
+      mma_commit_in(el, bar(kBarVEmpty + vs));
+      if (++vs == kPgVSlots) {
+        vs = 0;
+        vp ^= 1u;
+      }
       return true;
     };
     while (ok && walk.left > 0) {
-      const int nt = walk.segment();
+      const int nt = __shfl_sync(0xffffffffu, walk.segment(), 0);
       if (!(ok = warp_wait(bar(kBarQFull), uint32_t(seg & 1)))) break;
       tc_fence_after();
 #pragma unroll 1
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint8_t* src[4];
     auto rows = [&](int n) {
       const int rb = n % kPgRows;
-      if (!group_wait(2, kPgVWarp, bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u)) return false;
+      if (!warp_wait(bar(kBarRowFull + rb), uint32_t(n / kPgRows) & 1u)) return false;
       const int* row_s = reinterpret_cast<const int*>(keys_of(n)) + r0;
       any = row_s[0] >= 0;
 #pragma unroll
@@ -554,14 +561,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarRowEmpty + rb));
       return true;
     };
-    auto widen = [&](const uint4 (&w)[4], int sl, uint32_t parity) {  // into slot `sl`
-      if (!group_wait(2, kPgVWarp, bar(kBarVEmpty + sl), parity)) return false;
-      uint8_t* d = dst + sl * 2 * kPgSlot;
+    int vs = 0;
+    uint32_t vp = 0;
+    auto widen = [&](const uint4 (&w)[4]) {  // into the next slot
+      if (!warp_wait(bar(kBarVEmpty + vs), vp ^ 1u)) return false;
+      uint8_t* d = dst + vs * 2 * kPgSlot;
 #pragma unroll
       for (int j = 0; j < 4; ++j) store_fp16(d + j * 4096 + seg0, d + j * 4096 + seg1, w[j]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarVFull + sl));
+      if (lane == 0) mbar_arrive(bar(kBarVFull + vs));
+      if (++vs == kPgVSlots) {
+        vs = 0;
+        vp ^= 1u;
+      }
       return true;
     };
     // The codes of a slot are loaded two slots ahead, across tiles and rows.
@@ -572,18 +585,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
 #pragma unroll 1
     for (int i = 0; i < 2 * total && ok; ++i) {  // half a tile: 256 dims
-      const uint32_t parity = uint32_t(i & 1) ^ 1u;
-      if (!(ok = widen(w0, 0, parity))) break;
+      if (!(ok = widen(w0))) break;
       const bool more = i + 1 < 2 * total;
       const int col = (i & 1) ? 0 : 256;
       if (more) {
         if ((i & 1) && !(ok = rows((i + 1) >> 1))) break;
         load_codes(w0, src, col, any);
       }
-      if (!(ok = widen(w1, 1, parity))) break;
+      if (!(ok = widen(w1))) break;
       if (more) load_codes(w1, src, col + 128, any);
     }
-    if (!ok && vt == 0) raise_status(kStatusTimeout);
+    if (!ok && lane == 0) raise_status(kStatusTimeout);
   } else {
     // ---------------------------------------------------------------- softmax and queries
     const int st = threadIdx.x - 32 * kPgSoft;
@@ -674,7 +686,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // Of this head and 32 keys: x = y + off = y - m + kPgShift, y = S log2(e) + k (-inf where there is no key).  k and
         // m are whole numbers, so x takes one rounding, of its own size (before there is an m, off is -k of the tile's
         // first key).  Some x above kPgShift + kPgLazy, or a first maximum: the heads' maxima give a new m.
-        if (!(ok = group_wait(1, kPgSoft, bar(kBarSFull), uint32_t(n) & 1u))) break;
+        if (!(ok = group_wait(bar(kBarSFull), uint32_t(n) & 1u))) break;
         tc_fence_after();
         const float* cs_s = reinterpret_cast<const float*>(keys_of(n)) + 128 + key0;
         if (m == -INFINITY) {
@@ -728,7 +740,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
         }
         // P and O are free once the previous value product is done
-        if (t > 0 && !(ok = group_wait(1, kPgSoft, bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
+        if (t > 0 && !(ok = group_wait(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
         if (resc) {
           tc_fence_after();
           // O^T (lane = dim, column = head) *= alpha[head], where a head of these 16 asks for it
@@ -786,10 +798,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       walk.advance(nt);
       if (walk.left > 0) {
-        if (!ok || !(ok = group_wait(1, kPgSoft, bar(kBarQEmpty), uint32_t(seg & 1)))) break;
+        if (!ok || !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg & 1)))) break;
         query(walk.t);
       }
-      if (!ok || !(ok = group_wait(1, kPgSoft, bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
+      if (!ok || !(ok = group_wait(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
       tc_fence_after();
       float l, l1;
       f2_unpack(l2, l, l1);
