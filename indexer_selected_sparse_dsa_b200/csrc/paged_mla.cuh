@@ -34,7 +34,8 @@
 //  * warps 0 and 1 copy the tile's rows with cp.async, four chunks of 128 codes and
 //    the rope chunk, each 128 bytes of 128 keys;
 //  * warps 4..11 read the codes again (they are in L2 by then), widen them to
-//    fp16 and store them for the value product: two slots of 128 keys x 128 dims;
+//    fp16 and store them for the value product, three slots of 128 keys x 128 dims;
+//    at the end of a row they write its result;
 //  * warps 12..19 are the softmax (a thread: one head, 32 keys) and prepare the
 //    next row's query while the last value product of a row runs;
 //  * warp 2 issues S = Q K^T (M = 64 heads x (hi, lo), N = 128 keys) one tile
@@ -69,10 +70,10 @@ constexpr int kPgK = kPgP + kPgSlot;
 constexpr int kPgV = kPgK + kPgKSlots * kPgSlot;             // a slot: two chunks of 128 keys x 64 dims fp16
 constexpr int kPgKeyOff = kPgV + kPgVSlots * 2 * kPgSlot;    // of 128 keys: int row, float 2^k scale log2(e), k, 2^-k
 constexpr int kPgRedOff = kPgKeyOff + kPgRows * 2048;        // float red[2][64]
-constexpr int kPgMOff = kPgRedOff + 512;                     // float m[64], alpha[64], l[64], 2^e[64]
+constexpr int kPgMOff = kPgRedOff + 512;                     // float alpha[64], 1 / l [64], 2^e[64]
 constexpr int kPgBarOff = kPgMOff + 1024;
 enum PgBar {
-  kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarSFull, kBarSFree, kBarDrain,
+  kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarSFull, kBarSFree, kBarLFull, kBarDrain,
   kBarKFull, kBarKEmpty = kBarKFull + kPgKGroups, kBarVFull = kBarKEmpty + kPgKGroups,
   kBarVEmpty = kBarVFull + kPgVSlots, kBarRowFull = kBarVEmpty + kPgVSlots, kBarRowEmpty = kBarRowFull + kPgRows,
   kPgBars = kBarRowEmpty + kPgRows
@@ -176,23 +177,22 @@ __device__ __forceinline__ void store_fp16(uint8_t* s0, uint8_t* s1, const uint4
   *reinterpret_cast<uint4*>(s1) = make_uint4(f[4], f[5], f[6], f[7]);
 }
 
-// Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.  An infinite value
-// becomes NaN (codes have no infinity), and with it every score of the head.
-__device__ __forceinline__ void split_codes(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
+// Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.
+__device__ __forceinline__ void split_codes(uint32_t w0, uint32_t w1, f32x2 inv, uint32_t& hi, uint32_t& lo) {
   const uint32_t w[2] = {w0, w1};
-  hi = lo = 0;
+  uint32_t c[2], d[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    float a = __uint_as_float(w[p] << 16) * inv, b = __uint_as_float(w[p] & 0xffff0000u) * inv;
-    if (isinf(a)) a = __uint_as_float(0x7fc00000u);
-    if (isinf(b)) b = __uint_as_float(0x7fc00000u);
-    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c), __NV_E4M3)));
-    const uint32_t d =
-        __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (b - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-    hi |= c << (16 * p);
-    lo |= d << (16 * p);
+    const f32x2 v = f2_mul(f2_pack(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)), inv);
+    float a, b;
+    f2_unpack(v, a, b);
+    c[p] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c[p]), __NV_E4M3)));
+    f2_unpack(f2_fma(f2_pack(f.x, f.y), f2_pack(-16.f, -16.f), f2_mul(v, f2_pack(16.f, 16.f))), a, b);
+    d[p] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   }
+  hi = __byte_perm(c[0], c[1], 0x5410);
+  lo = __byte_perm(d[0], d[1], 0x5410);
 }
 
 template <bool kSparse>
@@ -206,10 +206,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + kPgBarOff + 8u * i; };
   auto keys_of = [&](int n) { return smem + kPgKeyOff + (n % kPgRows) * 2048; };  // the table of the CTA's tile n
-  float* m_s = reinterpret_cast<float*>(smem + kPgMOff);
-  float* alpha_s = m_s + 64;
-  float* l_s = m_s + 128;
-  float* g_s = m_s + 192;
+  float* alpha_s = reinterpret_cast<float*>(smem + kPgMOff);
+  float* linv_s = alpha_s + 64;
+  float* g_s = alpha_s + 128;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
   int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile, tiles of this CTA, tiles of a share
   // (by a shuffle, so that the compiler knows it to be the same in all lanes: the roles' addresses and descriptors
@@ -226,6 +225,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     mbar_init(bar(kBarCodes), 1);
     mbar_init(bar(kBarSFull), 1);
     mbar_init(bar(kBarSFree), 8);
+    mbar_init(bar(kBarLFull), 8);
     mbar_init(bar(kBarDrain), 1);
     for (int i = 0; i < kPgKGroups; ++i) {
       mbar_init(bar(kBarKFull + i), 64);  // every copying thread
@@ -548,6 +548,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint8_t* base = c.kv8 + 16 * g;
     uint8_t* const dst = smem + kPgV + voff;
     const int total = walk.left;
+    int seg = 0, i = 0;  // rows begun, half tiles (256 dims) done
+    int2 split = make_int2(-1, 0);
     bool ok = true, any = false;
     const uint8_t* src[4];
     auto rows = [&](int n) {
@@ -583,18 +585,60 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       load_codes(w0, src, 0, any);
       load_codes(w1, src, 128, any);
     }
-#pragma unroll 1
-    for (int i = 0; i < 2 * total && ok; ++i) {  // half a tile: 256 dims
-      if (!(ok = widen(w0))) break;
-      const bool more = i + 1 < 2 * total;
-      const int col = (i & 1) ? 0 : 256;
-      if (more) {
-        if ((i & 1) && !(ok = rows((i + 1) >> 1))) break;
-        load_codes(w0, src, col, any);
+    while (ok && walk.left > 0) {
+      const int nt = walk.segment(), row = walk.t, tile = walk.tile;
+      const bool whole = nt == walk.ntiles;
+      if (!whole && tile == 0) {
+        const int rest = walk.ntiles - nt, share = start_s[4];
+        split = make_int2(row, 1 + (rest + share - 1) / share);
       }
-      if (!(ok = widen(w1))) break;
-      if (more) load_codes(w1, src, col + 128, any);
+      walk.advance(nt);
+      const int end = i + 2 * nt;
+#pragma unroll 1
+      for (; i < end; ++i) {
+        if (!(ok = widen(w0))) break;
+        const bool more = i + 1 < 2 * total;
+        const int col = (i & 1) ? 0 : 256;
+        if (more) {
+          if ((i & 1) && !(ok = rows((i + 1) >> 1))) break;
+          load_codes(w0, src, col, any);
+        }
+        if (!(ok = widen(w1))) break;
+        if (more) load_codes(w1, src, col + 128, any);
+      }
+      // --- the row's result, or this part's.  O^T: a lane per dim, a column per head.
+      if (!ok || !(ok = warp_wait(bar(kBarLFull), uint32_t(seg & 1)))) break;
+      if (!(ok = warp_wait(bar(kBarPFree), uint32_t((end >> 1) - 1) & 1u))) break;
+      tc_fence_after();
+      const int quarter = warp & 3, h0 = 32 * ((warp - kPgVWarp) >> 2), odd = lane & 1;
+      // a CTA leaves at most two partial results: of the row it starts inside (0) and of the row it ends inside (1)
+      float* prow = part_out + (long long)(2 * blockIdx.x + (tile == 0 ? 1 : 0)) * kPartFloats + h0 * 512 + 32 * quarter + lane;
+      __nv_bfloat16* orow = o_lat + ((long long)row * 64 + h0 + odd) * 512 + 32 * quarter + (lane - odd);
+#pragma unroll 1
+      for (int mm = 0; mm < 4; ++mm) {
+        float ov[32];
+        tmem_ld32_sync((uint32_t(quarter * 32) << 16) + kPgOCol + 64 * mm + h0, ov);
+        if (whole) {
+          // two neighbouring lanes trade, so that each stores two dims of one head
+#pragma unroll
+          for (int h = 0; h < 32; h += 2) {
+            const float2 li = *reinterpret_cast<const float2*>(linv_s + h0 + h);
+            const float a = ov[h] * li.x, b = ov[h + 1] * li.y;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            *reinterpret_cast<__nv_bfloat162*>(orow + h * 512 + 128 * mm) =
+                __floats2bfloat162_rn(odd ? got : a, odd ? b : got);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 32; ++h) prow[h * 512 + 128 * mm] = ov[h];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOFree));
+      ++seg;
     }
+    if (vt == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
     if (!ok && lane == 0) raise_status(kStatusTimeout);
   } else {
     // ---------------------------------------------------------------- softmax and queries
@@ -623,22 +667,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         uint32_t amax = 0;
 #pragma unroll
         for (int j = 0; j < 9; ++j) {
-          const uint32_t a = (w[j] << 16) & 0x7fffffffu, b = w[j] & 0x7fff0000u;
-          if (a < 0x7f800000u) amax = max(amax, a);
-          if (b < 0x7f800000u) amax = max(amax, b);
+          amax = max(amax, max((w[j] << 16) & 0x7fffffffu, w[j] & 0x7fff0000u));
         }
         amax = __reduce_max_sync(0xffffffffu, amax);
         const int e = max(int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-        const float inv = pow2f(-e);
+        // an infinite or NaN value (codes have no infinity): every score of the head is NaN
+        const float inv = amax < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
         const int row = 32 * (h >> 4) + (h & 15);
         *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
             __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
-        if (lane == 0) g_s[h] = pow2f(e);
+        if (lane == 0) g_s[h] = amax < 0x7f800000u ? pow2f(e) : inv;
       }
       named_bar_sync(1, 256);
       // Codes: lane = row of the A operand.  The two lanes of a head split 16 dims, each makes hi and lo of its eight
       // and they trade: the hi lane ends with 16 hi codes, the lo lane with 16 lo codes.
       const float inv = 1.f / g_s[head];
+      const f32x2 inv2 = f2_pack(inv, inv);
       const uint16_t* qh = qt + head * 576 + 256 * w2 + 8 * part;
 #pragma unroll 2
       for (int i = 0; i < 16; i += 4) {
@@ -649,8 +693,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t hi[2], lo[2];
-          split_codes(v[k].x, v[k].y, inv, hi[0], lo[0]);
-          split_codes(v[k].z, v[k].w, inv, hi[1], lo[1]);
+          split_codes(v[k].x, v[k].y, inv2, hi[0], lo[0]);
+          split_codes(v[k].z, v[k].w, inv2, hi[1], lo[1]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t mine = part ? lo[e] : hi[e];
@@ -674,7 +718,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           make_uint4(0, 0, 0, 0);
     query(walk.t);
     int n = 0, seg = 0;
-    int2 split = make_int2(-1, 0);
     while (ok && walk.left > 0) {  // (`ok` is the same in all threads of the role)
       const int nt = walk.segment();
       const float g = g_s[head];
@@ -789,67 +832,35 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           mbar_arrive(bar(kBarPFull));
         }
       }
-      // --- the next row's query, then this row's (or this part's) result
-      const int row = walk.t, tile = walk.tile;
-      const bool whole = nt == walk.ntiles;
-      if (!whole && tile == 0) {
-        const int rest = walk.ntiles - nt, share = start_s[4];
-        split = make_int2(row, 1 + (rest + share - 1) / share);
-      }
-      walk.advance(nt);
-      if (walk.left > 0) {
-        if (!ok || !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg & 1)))) break;
-        query(walk.t);
-      }
-      if (!ok || !(ok = group_wait(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
-      tc_fence_after();
+      // --- the row's sum: its reciprocal for the value role, which writes the result; then the next row's query
+      if (!ok || (seg > 0 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u)))) break;
       float l, l1;
       f2_unpack(l2, l, l1);
       l += l1;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       if (part == 0) red[64 * w2 + head] = l;
       named_bar_sync(1, 256);
-      if (sw < 4 && part == 0) {
+      if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
         l = red[head] + red[64 + head];
-        l_s[head] = l;
-        m_s[head] = m;  // (l is 0 or NaN where there is no m)
-      }
-      named_bar_sync(1, 256);
-      // a CTA leaves at most two partial results: of the row it starts inside (0) and of the row it ends inside (1)
-      float* prow = part_out + (long long)(2 * blockIdx.x + (tile == 0 ? 1 : 0)) * kPartFloats;
-#pragma unroll 1
-      for (int mm = 0; mm < 4; ++mm) {
-        float ov[32];
-        tmem_ld32_sync(lane_addr + kPgOCol + 64 * mm + h0, ov);
-        const int d = 128 * mm + 32 * quarter + lane;
-#pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          if (whole) {
-            const float lh = l_s[h0 + h];
-            o_lat[((long long)row * 64 + h0 + h) * 512 + d] = __float2bfloat16(lh == 0.f ? 0.f : ov[h] / lh);
-          } else {
-            prow[(h0 + h) * 512 + d] = ov[h];
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarOFree));
-      if (st < 64) {
-        const float lh = l_s[st], mh = m_s[st];
-        if (!whole) {
-          prow[64 * 512 + st] = mh;
-          prow[64 * 512 + 64 + st] = lh;
+        linv_s[head] = l == 0.f ? 0.f : 1.f / l;
+        if (nt != walk.ntiles) {
+          float* prow = part_out + (long long)(2 * blockIdx.x + (walk.tile == 0 ? 1 : 0)) * kPartFloats + 64 * 512;
+          prow[head] = m;
+          prow[64 + head] = l;
         } else if (lse) {
-          lse[(long long)row * 64 + st] = lh == 0.f ? -INFINITY : (mh - kPgShift + log2f(lh)) * 0.69314718055994531f;
+          lse[(long long)walk.t * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
         }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarLFull));
+      walk.advance(nt);
+      if (walk.left > 0) {
+        if (!(ok = group_wait(bar(kBarQEmpty), uint32_t(seg & 1)))) break;
+        query(walk.t);
       }
       ++seg;
     }
-    if (st == 0) {
-      if (!ok) raise_status(kStatusTimeout);
-      meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
-    }
+    if (!ok && st == 0) raise_status(kStatusTimeout);
   }
   pdl_trigger();
   tc_fence_before();
