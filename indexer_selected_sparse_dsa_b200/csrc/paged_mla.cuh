@@ -70,8 +70,9 @@ constexpr int kPgK = kPgP + kPgSlot;
 constexpr int kPgV = kPgK + kPgKSlots * kPgSlot;             // a slot: two chunks of 128 keys x 64 dims fp16
 constexpr int kPgKeyOff = kPgV + kPgVSlots * 2 * kPgSlot;    // of 128 keys: int row, float 2^k scale log2(e), k, 2^-k
 constexpr int kPgRedOff = kPgKeyOff + kPgRows * 2048;        // float red[2][64]
-constexpr int kPgMOff = kPgRedOff + 512;                     // float alpha[64], 1 / l [64], 2^e[64]
-constexpr int kPgBarOff = kPgMOff + 1024;
+constexpr int kPgMOff = kPgRedOff + 512;                     // float alpha[64], 1 / l [64], 2^-e[64]
+constexpr int kPgStageOff = kPgMOff + 768;                   // codes of 64 dims on their way to tensor memory: 128 rows x 64
+constexpr int kPgBarOff = kPgStageOff + 8192;
 enum PgBar {
   kBarQFull, kBarQEmpty, kBarPFull, kBarPFree, kBarOFree, kBarCodes, kBarSFull, kBarSFree, kBarLFull, kBarDrain,
   kBarKFull, kBarKEmpty = kBarKFull + kPgKGroups, kBarVFull = kBarKEmpty + kPgKGroups,
@@ -177,19 +178,31 @@ __device__ __forceinline__ void store_fp16(uint8_t* s0, uint8_t* s1, const uint4
   *reinterpret_cast<uint4*>(s1) = make_uint4(f[4], f[5], f[6], f[7]);
 }
 
-// Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.
+// The largest magnitudes of eight bf16, even and odd ones apart (as patterns: they order like the values).
+__device__ __forceinline__ uint32_t max_abs_bf16(const uint4& x) {
+  return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, f32x2 inv) {
+  float a, b;
+  f2_unpack(f2_mul(f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), inv), a, b);
+  const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&o);
+}
+
+// Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.  v goes through
+// fp16, exact but for what is 2^-33 of 448.
 __device__ __forceinline__ void split_codes(uint32_t w0, uint32_t w1, f32x2 inv, uint32_t& hi, uint32_t& lo) {
   const uint32_t w[2] = {w0, w1};
   uint32_t c[2], d[2];
+  const __half2 n16 = __half2half2(__ushort_as_half(0xcc00)), p16 = __half2half2(__ushort_as_half(0x4c00));  // -16, 16
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const f32x2 v = f2_mul(f2_pack(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)), inv);
     float a, b;
-    f2_unpack(v, a, b);
-    c[p] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c[p]), __NV_E4M3)));
-    f2_unpack(f2_fma(f2_pack(f.x, f.y), f2_pack(-16.f, -16.f), f2_mul(v, f2_pack(16.f, 16.f))), a, b);
-    d[p] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)), inv), a, b);
+    const __half2 v = __floats2half2_rn(a, b);
+    c[p] = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    const __half2 f(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(c[p]), __NV_E4M3));
+    d[p] = __nv_cvt_halfraw2_to_fp8x2(__hfma2(f, n16, __hmul2(v, p16)), __NV_SATFINITE, __NV_E4M3);
   }
   hi = __byte_perm(c[0], c[1], 0x5410);
   lo = __byte_perm(d[0], d[1], 0x5410);
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   auto keys_of = [&](int n) { return smem + kPgKeyOff + (n % kPgRows) * 2048; };  // the table of the CTA's tile n
   float* alpha_s = reinterpret_cast<float*>(smem + kPgMOff);
   float* linv_s = alpha_s + 64;
-  float* g_s = alpha_s + 128;
+  float* qinv_s = alpha_s + 128;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
   int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile, tiles of this CTA, tiles of a share
   // (by a shuffle, so that the compiler knows it to be the same in all lanes: the roles' addresses and descriptors
@@ -652,79 +665,125 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     float* red = reinterpret_cast<float*>(smem + kPgRedOff);
     bool ok = true;
 
-    // The query of row `t` into tensor memory (codes) and shared memory (rope half).
-    auto query = [&](int t) {
-      const uint16_t* qt = q + (long long)t * 64 * 576;
-      // each head's largest value, a warp per head: 2^e with max |q| <= 448 2^e, and the rope half by it
-#pragma unroll 4
-      for (int i = 0; i < 8; ++i) {
-        const int h = 8 * sw + i;
-        const uint16_t* qh = qt + h * 576;
-        const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 16 * lane);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(qh + 16 * lane + 8);
+    // the lo rows of the rope half stay zero
+    for (int i = st; i < 64 * 8; i += 256)
+      *reinterpret_cast<uint4*>(smem + kPgQR + (32 * (i >> 7) + 16 + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+    int n = 0, seg = 0;
+    // the head's running maximum m of y (a whole number) and sum (two keys side by side); the row they are of
+    float m = -INFINITY;
+    f32x2 l2 = 0ull;
+    int row = 0;
+    bool whole = false, head_part = false;
+    // 2^-e of four of this warp's heads of query row t, max |q| <= 448 2^e: done for the next row while the softmax waits
+    // for scores.  An infinite or NaN value (codes have no infinity) makes all of the head's codes NaN.
+    int scaled = 0;
+    auto scale_heads = [&](int t) {
+      uint32_t amax[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* qh = q + ((long long)t * 64 + 8 * sw + 4 * scaled + i) * 576;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 8 * lane), x1 = *reinterpret_cast<const uint4*>(qh + 256 + 8 * lane);
         const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
-        const uint32_t w[9] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w, xr};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 9; ++j) {
-          amax = max(amax, max((w[j] << 16) & 0x7fffffffu, w[j] & 0x7fff0000u));
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const int e = max(int(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-        // an infinite or NaN value (codes have no infinity): every score of the head is NaN
-        const float inv = amax < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
-        const int row = 32 * (h >> 4) + (h & 15);
-        *reinterpret_cast<__nv_bfloat162*>(smem + kPgQR + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) =
-            __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
-        if (lane == 0) g_s[h] = amax < 0x7f800000u ? pow2f(e) : inv;
+        amax[i] = __vmaxu2(__vmaxu2(max_abs_bf16(x0), max_abs_bf16(x1)), xr & 0x7fff7fffu);
       }
-      named_bar_sync(1, 256);
-      // Codes: lane = row of the A operand.  The two lanes of a head split 16 dims, each makes hi and lo of its eight
-      // and they trade: the hi lane ends with 16 hi codes, the lo lane with 16 lo codes.
-      const float inv = 1.f / g_s[head];
-      const f32x2 inv2 = f2_pack(inv, inv);
-      const uint16_t* qh = qt + head * 576 + 256 * w2 + 8 * part;
-#pragma unroll 2
-      for (int i = 0; i < 16; i += 4) {
-        uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(qh + 16 * (i + k));
-        float f[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t hi[2], lo[2];
-          split_codes(v[k].x, v[k].y, inv2, hi[0], lo[0]);
-          split_codes(v[k].z, v[k].w, inv2, hi[1], lo[1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t mine = part ? lo[e] : hi[e];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, part ? hi[e] : lo[e], 16);
-            f[4 * k + e] = __uint_as_float(part ? got : mine);
-            f[4 * k + 2 + e] = __uint_as_float(part ? mine : got);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __reduce_max_sync(0xffffffffu, max(amax[i] << 16, amax[i] & 0xffff0000u));
+        const int e = max(int(a >> 23) - 135 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+        if (lane == 0) qinv_s[8 * sw + 4 * scaled + i] = a < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
+      }
+      ++scaled;
+    };
+    for (;;) {  // (`ok` is the same in all threads of the role)
+      const bool more = walk.left > 0;
+      // --- the sum of the row before: its reciprocal for the value role, which writes the result
+      if (seg > 0) {
+        if (!ok || (seg > 1 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg) & 1u)))) break;
+        float l, l1;
+        f2_unpack(l2, l, l1);
+        l += l1;
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (part == 0) red[64 * w2 + head] = l;
+        named_bar_sync(1, 256);
+        if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
+          l = red[head] + red[64 + head];
+          linv_s[head] = l == 0.f ? 0.f : 1.f / l;
+          if (!whole) {
+            float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
+            prow[head] = m;
+            prow[64 + head] = l;
+          } else if (lse) {
+            lse[(long long)row * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
           }
         }
-        tmem_st16(lane_addr + kPgQCol + 64 * w2 + 4 * i, f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarLFull));
+        if (more && !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg - 1) & 1u))) break;
+      }
+      if (!more) break;
+      // --- the query's codes into tensor memory (lane = row of the A operand), 64 dims a step through shared memory, and
+      // the rope half (the ninth step) into shared memory.  A step: eight lanes read 128 bytes of a head.
+      while (scaled < 2) scale_heads(walk.t);
+      named_bar_sync(1, 256);
+      scaled = 0;
+      const float own = qinv_s[head], g = own == own ? 1.f / own : 1.f;
+      const f32x2 g2 = f2_pack(g, g);
+      {
+        const int hd = 8 * sw + (lane >> 3);  // and hd + 4
+        const uint4* src = reinterpret_cast<const uint4*>(q + ((long long)walk.t * 64 + hd) * 576) + (lane & 7);
+        uint4 v0 = src[0], v1 = src[4 * 72];
+        const float i0 = qinv_s[hd], i1 = qinv_s[hd + 4];
+        const f32x2 inv[2] = {f2_pack(i0, i0), f2_pack(i1, i1)};
+        const int own_row = 32 * quarter + lane;
+        uint8_t* stage = smem + kPgStageOff;
+#pragma unroll 1
+        for (int i = 0; i < 9; ++i) {
+          const uint4 x[2] = {v0, v1};
+          if (i < 8) {
+            v0 = src[8 * (i + 1)];
+            v1 = src[8 * (i + 1) + 4 * 72];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int h = hd + 4 * k, row = 32 * (h >> 4) + (h & 15);
+            if (i < 8) {
+              uint2 hi, lo;
+              split_codes(x[k].x, x[k].y, inv[k], hi.x, lo.x);
+              split_codes(x[k].z, x[k].w, inv[k], hi.y, lo.y);
+              const int at = 16 * (((lane & 7) >> 1) ^ ((row >> 1) & 3)) + 8 * (lane & 1);  // (row + 16 has the same swizzle)
+              *reinterpret_cast<uint2*>(stage + row * 64 + at) = hi;
+              *reinterpret_cast<uint2*>(stage + (row + 16) * 64 + at) = lo;
+            } else {
+              *reinterpret_cast<uint4*>(smem + kPgQR + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(scale_bf16x2(x[k].x, inv[k]), scale_bf16x2(x[k].y, inv[k]), scale_bf16x2(x[k].z, inv[k]),
+                             scale_bf16x2(x[k].w, inv[k]));
+            }
+          }
+          if (i == 8) break;
+          named_bar_sync(1, 256);
+          uint4 c[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            c[k] = *reinterpret_cast<const uint4*>(stage + own_row * 64 + 16 * ((2 * w2 + k) ^ ((own_row >> 1) & 3)));
+          tmem_st8(lane_addr + kPgQCol + 16 * i + 8 * w2, reinterpret_cast<const uint32_t*>(c));
+          named_bar_sync(1, 256);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarQFull));
-    };
 
-    // the lo rows of the rope half stay zero
-    for (int i = st; i < 64 * 8; i += 256)
-      *reinterpret_cast<uint4*>(smem + kPgQR + (32 * (i >> 7) + 16 + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
-    query(walk.t);
-    int n = 0, seg = 0;
-    while (ok && walk.left > 0) {  // (`ok` is the same in all threads of the role)
       const int nt = walk.segment();
-      const float g = g_s[head];
-      const f32x2 g2 = f2_pack(g, g);
-      // the head's running maximum m of y (a whole number), off = kPgShift - m, and the x that asks for a new one
-      float m = -INFINITY, off = 0.f, most = -INFINITY;
-      f32x2 l2 = 0ull;
+      row = walk.t;
+      whole = nt == walk.ntiles;
+      head_part = walk.tile == 0;
+      walk.advance(nt);
+      float off = 0.f, most = -INFINITY;  // kPgShift - m, and the x that asks for a new m
+      m = -INFINITY;
+      l2 = 0ull;
       for (int t = 0; t < nt; ++t, ++n) {
         // Of this head and 32 keys: x = y + off = y - m + kPgShift, y = S log2(e) + k (-inf where there is no key).  k and
         // m are whole numbers, so x takes one rounding, of its own size (before there is an m, off is -k of the tile's
@@ -831,32 +890,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           mbar_arrive(bar(kBarRowEmpty + n % kPgRows));
           mbar_arrive(bar(kBarPFull));
         }
-      }
-      // --- the row's sum: its reciprocal for the value role, which writes the result; then the next row's query
-      if (!ok || (seg > 0 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg - 1) & 1u)))) break;
-      float l, l1;
-      f2_unpack(l2, l, l1);
-      l += l1;
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (part == 0) red[64 * w2 + head] = l;
-      named_bar_sync(1, 256);
-      if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
-        l = red[head] + red[64 + head];
-        linv_s[head] = l == 0.f ? 0.f : 1.f / l;
-        if (nt != walk.ntiles) {
-          float* prow = part_out + (long long)(2 * blockIdx.x + (walk.tile == 0 ? 1 : 0)) * kPartFloats + 64 * 512;
-          prow[head] = m;
-          prow[64 + head] = l;
-        } else if (lse) {
-          lse[(long long)walk.t * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarLFull));
-      walk.advance(nt);
-      if (walk.left > 0) {
-        if (!(ok = group_wait(bar(kBarQEmpty), uint32_t(seg & 1)))) break;
-        query(walk.t);
+        if (walk.left > 0 && scaled < 2) scale_heads(walk.t);
       }
       ++seg;
     }
