@@ -254,95 +254,114 @@ def dsa_block_sparse_attn(q_I, w, k_I, q, kv, kv_start, n_vis, max_n_vis, gates,
                                        _ptr(lse), _ptr(blocks_out), _ptr(ws), ws.numel(), _stream(stream)))
 
 
-def _need_paged(seq_len, page_table, kv8, kv_scale, cu_q=None):
-    """Check the batch's description and the cache; (batch, max_pages, n_pages, page_size)."""
+# A decode step calls the paged entry points once per layer, so their checks are made for few Python calls: one pass
+# over (tensor, dtype, shape, name) with the common case tested in place, and plain integers to ctypes.
+
+def _device():
+    """The current device; None before there is any CUDA tensor (and so none to check)."""
     import torch
-    _need(seq_len, torch.int32, None, "seq_len")
-    batch = seq_len.numel()
-    _need(seq_len, torch.int32, (batch,), "seq_len")
-    if cu_q is not None:
-        _need(cu_q, torch.int32, (batch + 1,), "cu_q")
-    _need(kv8, torch.uint8, None, "kv8")
-    if kv8.dim() != 3 or kv8.shape[2] != ROW8:
-        raise ValueError(f"kv8 must have shape (n_pages, page_size, {ROW8}), got {tuple(kv8.shape)}")
-    _need(kv_scale, torch.float32, kv8.shape[:2], "kv_scale")
-    _need(page_table, torch.int32, None, "page_table")
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError(f"page_table must have shape ({batch}, max_pages), got {tuple(page_table.shape)}")
-    return batch, page_table.shape[1], kv8.shape[0], kv8.shape[1]
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
 
 
-def _on_current_device(*tensors):
-    """The kernels run on the current device: a tensor of another one would be a wild pointer to them."""
+def _check_all(dev, *specs):
+    """Check each (tensor, dtype, shape, name); None for an optional tensor.  Returns the addresses.
+
+    The kernels run on the current device `dev`: a tensor of another one would be a wild pointer to them."""
+    ptrs = []
+    for t, dtype, shape, name in specs:
+        if t is None:
+            ptrs.append(None)
+            continue
+        try:
+            good = t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+        except AttributeError:
+            good = False
+        if not good:
+            _need(t, dtype, shape, name)
+            raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _raw_stream(stream, dev):
     import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _paged_sizes(seq_len, page_table, kv8):
+    """(batch, max_pages, n_pages, page_size); a wrong number of dimensions is found here, wrong sizes by _check_all."""
+    for t, nd, name in ((seq_len, 1, "seq_len"), (page_table, 2, "page_table"), (kv8, 3, "kv8")):
+        if getattr(t, "ndim", None) != nd:
+            raise TypeError(f"{name} must be a tensor of {nd} dimension{'s' if nd > 1 else ''}")
+    return seq_len.shape[0], page_table.shape[1], kv8.shape[0], kv8.shape[1]
 
 
 def dsa_cache_write(rows, cu_q, seq_len, page_table, kv8, kv_scale, stream=None):
     """Quantise latent rows [T, 576] bf16 (their row stride is free, the rest contiguous)
     into the paged cache kv8 [n_pages, page_size, 640] uint8, kv_scale [n_pages, page_size]."""
     import torch
-    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
+    batch, max_pages, n_pages, page_size = _paged_sizes(seq_len, page_table, kv8)
+    i32, dev = torch.int32, _device()
+    cu, sl, pt, k8, ks = _check_all(
+        dev, (cu_q, i32, (batch + 1,), "cu_q"), (seq_len, i32, (batch,), "seq_len"),
+        (page_table, i32, (batch, max_pages), "page_table"), (kv8, torch.uint8, (n_pages, page_size, ROW8), "kv8"),
+        (kv_scale, torch.float32, (n_pages, page_size), "kv_scale"))
     if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype != torch.bfloat16:
         raise TypeError("rows must be a CUDA tensor of torch.bfloat16")
-    if rows.dim() != 2 or rows.shape[1] != ROW or rows.stride(1) != 1:
+    if rows.ndim != 2 or rows.shape[1] != ROW or rows.stride(1) != 1:
         raise ValueError(f"rows must have shape (T, {ROW}) with contiguous rows, got {tuple(rows.shape)}, "
                          f"strides {rows.stride()}")
-    _on_current_device(rows, cu_q, seq_len, page_table, kv8, kv_scale)
+    if rows.get_device() != dev:
+        raise ValueError(f"rows must be on the current device cuda:{dev}, got {rows.device}")
     T = rows.shape[0]
-    ld = rows.stride(0) if T > 1 else ROW
-    _check(lib().dsa_cache_write(_ptr(rows), ld, T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
-                                 _ptr(kv8), _ptr(kv_scale), n_pages, page_size, _stream(stream)))
+    _check(lib().dsa_cache_write(rows.data_ptr(), rows.stride(0) if T > 1 else ROW, T, cu, sl, pt, batch, max_pages, k8,
+                                 ks, n_pages, page_size, _raw_stream(stream, dev)))
 
 
 def dsa_cache_read(kv8, kv_scale, seq_len, page_table, kv_start, kv, stream=None):
     """Unpack every sequence of the paged cache to flat bf16 rows kv[kv_start[b] + s]."""
     import torch
-    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale)
-    _need(kv_start, torch.int64, (batch,), "kv_start")
-    _need(kv, torch.bfloat16, (kv.shape[0], ROW), "kv")
-    _on_current_device(kv8, kv_scale, seq_len, page_table, kv_start, kv)
-    _check(lib().dsa_cache_read(_ptr(kv8), _ptr(kv_scale), n_pages, page_size, _ptr(seq_len), _ptr(page_table), batch,
-                                max_pages, _ptr(kv_start), _ptr(kv), kv.shape[0], _stream(stream)))
+    batch, max_pages, n_pages, page_size = _paged_sizes(seq_len, page_table, kv8)
+    cache_rows = kv.shape[0]
+    i32, dev = torch.int32, _device()
+    k8, ks, sl, pt, start, flat = _check_all(
+        dev, (kv8, torch.uint8, (n_pages, page_size, ROW8), "kv8"),
+        (kv_scale, torch.float32, (n_pages, page_size), "kv_scale"), (seq_len, i32, (batch,), "seq_len"),
+        (page_table, i32, (batch, max_pages), "page_table"), (kv_start, torch.int64, (batch,), "kv_start"),
+        (kv, torch.bfloat16, (cache_rows, ROW), "kv"))
+    _check(lib().dsa_cache_read(k8, ks, n_pages, page_size, sl, pt, batch, max_pages, start, flat, cache_rows,
+                                _raw_stream(stream, dev)))
 
 
-def _need_paged_attn(q, o_lat, lse, ws):
+def _paged_attn(name, q, cu_q, seq_len, page_table, idx, kv8, kv_scale, scale, o_lat, lse, ws, stream):
     import torch
-    T = q.shape[0]
-    _need(q, torch.bfloat16, (T, HEADS, ROW), "q")
-    _need(o_lat, torch.bfloat16, (T, HEADS, LATENT), "o_lat")
-    if lse is not None:
-        _need(lse, torch.float32, (T, HEADS), "lse")
-    _need(ws, torch.uint8, None, "ws")
-    return T
+    batch, max_pages, n_pages, page_size = _paged_sizes(seq_len, page_table, kv8)
+    i32, f32, bf16, dev, T = torch.int32, torch.float32, torch.bfloat16, _device(), q.shape[0]
+    qp, cu, sl, pt, k8, ks, op, lp, wp = _check_all(
+        dev, (q, bf16, (T, HEADS, ROW), "q"), (cu_q, i32, (batch + 1,), "cu_q"), (seq_len, i32, (batch,), "seq_len"),
+        (page_table, i32, (batch, max_pages), "page_table"), (kv8, torch.uint8, (n_pages, page_size, ROW8), "kv8"),
+        (kv_scale, f32, (n_pages, page_size), "kv_scale"), (o_lat, bf16, (T, HEADS, LATENT), "o_lat"),
+        (lse, f32, (T, HEADS), "lse"), (ws, torch.uint8, (ws.numel(),), "ws"))
+    sel = ()
+    if idx is not None:
+        if getattr(idx, "ndim", None) != 2:
+            raise TypeError("idx must be a tensor of 2 dimensions")
+        sel = (*_check_all(dev, (idx, i32, (T, idx.shape[1]), "idx")), idx.shape[1])
+    _check(getattr(lib(), name)(qp, T, cu, sl, pt, batch, max_pages, *sel, k8, ks, n_pages, page_size, scale, op, lp, wp,
+                                ws.numel(), _raw_stream(stream, dev)))
 
 
 def dsa_paged_mla_attn(q, cu_q, seq_len, page_table, kv8, kv_scale, scale, o_lat, lse, ws, stream=None):
     """Dense latent attention of the new tokens over their sequences' pages; o_lat is bf16, lse may be None."""
-    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
-    T = _need_paged_attn(q, o_lat, lse, ws)
-    _on_current_device(q, cu_q, seq_len, page_table, kv8, kv_scale, o_lat, lse, ws)
-    _check(lib().dsa_paged_mla_attn(_ptr(q), T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
-                                    _ptr(kv8), _ptr(kv_scale), n_pages, page_size, float(scale), _ptr(o_lat),
-                                    _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    _paged_attn("dsa_paged_mla_attn", q, cu_q, seq_len, page_table, None, kv8, kv_scale, scale, o_lat, lse, ws, stream)
 
 
 def dsa_paged_sparse_mla_attn(q, cu_q, seq_len, page_table, idx, kv8, kv_scale, scale, o_lat, lse, ws, stream=None):
     """Latent attention of the new tokens over their selected positions idx [T, topk] of the paged cache."""
-    import torch
-    batch, max_pages, n_pages, page_size = _need_paged(seq_len, page_table, kv8, kv_scale, cu_q)
-    T = _need_paged_attn(q, o_lat, lse, ws)
-    _need(idx, torch.int32, None, "idx")
-    if idx.dim() != 2 or idx.shape[0] != T:
-        raise ValueError(f"idx must have shape ({T}, topk), got {tuple(idx.shape)}")
-    _on_current_device(q, cu_q, seq_len, page_table, idx, kv8, kv_scale, o_lat, lse, ws)
-    _check(lib().dsa_paged_sparse_mla_attn(_ptr(q), T, _ptr(cu_q), _ptr(seq_len), _ptr(page_table), batch, max_pages,
-                                           _ptr(idx), idx.shape[1], _ptr(kv8), _ptr(kv_scale), n_pages, page_size,
-                                           float(scale), _ptr(o_lat), _ptr(lse), _ptr(ws), ws.numel(),
-                                           _stream(stream)))
+    if idx is None:
+        raise TypeError("idx must be a CUDA tensor")
+    _paged_attn("dsa_paged_sparse_mla_attn", q, cu_q, seq_len, page_table, idx, kv8, kv_scale, scale, o_lat, lse, ws,
+                stream)
 
 
 def dsa_sync_status(stream=None):

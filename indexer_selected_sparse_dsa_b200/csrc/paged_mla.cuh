@@ -669,118 +669,129 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     for (int i = st; i < 64 * 8; i += 256)
       *reinterpret_cast<uint4*>(smem + kPgQR + (32 * (i >> 7) + 16 + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
           make_uint4(0, 0, 0, 0);
-    int n = 0, seg = 0;
+    int n = 0, seg = -1, nt = 0;  // tiles done, rows begun before this one
+    float g = 1.f;                // 2^e of the head's query
     // the head's running maximum m of y (a whole number) and sum (two keys side by side); the row they are of
     float m = -INFINITY;
     f32x2 l2 = 0ull;
     int row = 0;
     bool whole = false, head_part = false;
-    // 2^-e of four of this warp's heads of query row t, max |q| <= 448 2^e: done for the next row while the softmax waits
-    // for scores.  An infinite or NaN value (codes have no infinity) makes all of the head's codes NaN.
-    int scaled = 0;
-    auto scale_heads = [&](int t) {
-      uint32_t amax[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint16_t* qh = q + ((long long)t * 64 + 8 * sw + 4 * scaled + i) * 576;
-        const uint4 x0 = *reinterpret_cast<const uint4*>(qh + 8 * lane), x1 = *reinterpret_cast<const uint4*>(qh + 256 + 8 * lane);
-        const uint32_t xr = *reinterpret_cast<const uint32_t*>(qh + 512 + 2 * lane);
-        amax[i] = __vmaxu2(__vmaxu2(max_abs_bf16(x0), max_abs_bf16(x1)), xr & 0x7fff7fffu);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = __reduce_max_sync(0xffffffffu, max(amax[i] << 16, amax[i] & 0xffff0000u));
-        const int e = max(int(a >> 23) - 135 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-        if (lane == 0) qinv_s[8 * sw + 4 * scaled + i] = a < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
-      }
-      ++scaled;
-    };
-    for (;;) {  // (`ok` is the same in all threads of the role)
+    for (;; ++seg) {  // (`ok` is the same in all threads of the role)
       const bool more = walk.left > 0;
-      // --- the sum of the row before: its reciprocal for the value role, which writes the result
-      if (seg > 0) {
-        if (!ok || (seg > 1 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg) & 1u)))) break;
-        float l, l1;
-        f2_unpack(l2, l, l1);
-        l += l1;
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (part == 0) red[64 * w2 + head] = l;
-        named_bar_sync(1, 256);
-        if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
-          l = red[head] + red[64 + head];
-          linv_s[head] = l == 0.f ? 0.f : 1.f / l;
-          if (!whole) {
-            float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
-            prow[head] = m;
-            prow[64 + head] = l;
-          } else if (lse) {
-            lse[(long long)row * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
+      if (seg >= 0) {
+        // --- the sum of the row before: its reciprocal for the value role, which writes the result
+        if (seg > 0) {
+          if (!ok || (seg > 1 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg) & 1u)))) break;
+          float l, l1;
+          f2_unpack(l2, l, l1);
+          l += l1;
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (part == 0) red[64 * w2 + head] = l;
+          named_bar_sync(1, 256);
+          if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
+            l = red[head] + red[64 + head];
+            linv_s[head] = l == 0.f ? 0.f : 1.f / l;
+            if (!whole) {
+              float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
+              prow[head] = m;
+              prow[64 + head] = l;
+            } else if (lse) {
+              lse[(long long)row * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
+            }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarLFull));
+          if (more && !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg - 1) & 1u))) break;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarLFull));
-        if (more && !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg - 1) & 1u))) break;
-      }
-      if (!more) break;
-      // --- the query's codes into tensor memory (lane = row of the A operand), 64 dims a step through shared memory, and
-      // the rope half (the ninth step) into shared memory.  A step: eight lanes read 128 bytes of a head.
-      while (scaled < 2) scale_heads(walk.t);
-      named_bar_sync(1, 256);
-      scaled = 0;
-      const float own = qinv_s[head], g = own == own ? 1.f / own : 1.f;
-      const f32x2 g2 = f2_pack(g, g);
-      {
-        const int hd = 8 * sw + (lane >> 3);  // and hd + 4
-        const uint4* src = reinterpret_cast<const uint4*>(q + ((long long)walk.t * 64 + hd) * 576) + (lane & 7);
-        uint4 v0 = src[0], v1 = src[4 * 72];
-        const float i0 = qinv_s[hd], i1 = qinv_s[hd + 4];
-        const f32x2 inv[2] = {f2_pack(i0, i0), f2_pack(i1, i1)};
-        const int own_row = 32 * quarter + lane;
-        uint8_t* stage = smem + kPgStageOff;
+        if (!more) break;
+        // --- the query's codes into tensor memory (lane = row of the A operand), 64 dims a step through shared memory, and
+        // the rope half (the ninth step) into shared memory.  A step: eight lanes read 128 bytes of a head.
+              named_bar_sync(1, 256);
+        const float own = qinv_s[head];
+        g = own == own ? 1.f / own : 1.f;
+        {
+          const int hd = 8 * sw + (lane >> 3);  // and hd + 4
+          const uint4* src = reinterpret_cast<const uint4*>(q + ((long long)walk.t * 64 + hd) * 576) + (lane & 7);
+          const float i0 = qinv_s[hd], i1 = qinv_s[hd + 4];
+          const f32x2 inv[2] = {f2_pack(i0, i0), f2_pack(i1, i1)};
+          const int own_row = 32 * quarter + lane;
+          uint8_t* stage = smem + kPgStageOff;
+          uint4 x[4], nx[4];  // dims 128 i .. + 63 of the two heads, then the next 64
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = src[8 * (k >> 1) + 288 * (k & 1)];
 #pragma unroll 1
-        for (int i = 0; i < 9; ++i) {
-          const uint4 x[2] = {v0, v1};
-          if (i < 8) {
-            v0 = src[8 * (i + 1)];
-            v1 = src[8 * (i + 1) + 4 * 72];
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nx[k] = src[min(16 * (i + 1), 56) + 8 * (k >> 1) + 288 * (k & 1)];
+            uint2 hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              split_codes(x[k].x, x[k].y, inv[k & 1], hi[k].x, lo[k].x);
+              split_codes(x[k].z, x[k].w, inv[k & 1], hi[k].y, lo[k].y);
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int h = hd + 4 * k, row = 32 * (h >> 4) + (h & 15);
+                const int at = 16 * (((lane & 7) >> 1) ^ ((row >> 1) & 3)) + 8 * (lane & 1);  // (of row + 16 too)
+                *reinterpret_cast<uint2*>(stage + row * 64 + at) = hi[2 * d + k];
+                *reinterpret_cast<uint2*>(stage + (row + 16) * 64 + at) = lo[2 * d + k];
+              }
+              named_bar_sync(1, 256);
+              uint4 c[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                c[k] = *reinterpret_cast<const uint4*>(stage + own_row * 64 + 16 * ((2 * w2 + k) ^ ((own_row >> 1) & 3)));
+              tmem_st8(lane_addr + kPgQCol + 32 * i + 16 * d + 8 * w2, reinterpret_cast<const uint32_t*>(c));
+              named_bar_sync(1, 256);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = nx[k];
           }
+          // (the last "next" is dims 448 .. 511 and, 64 further, the rope half)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int h = hd + 4 * k, row = 32 * (h >> 4) + (h & 15);
-            if (i < 8) {
-              uint2 hi, lo;
-              split_codes(x[k].x, x[k].y, inv[k], hi.x, lo.x);
-              split_codes(x[k].z, x[k].w, inv[k], hi.y, lo.y);
-              const int at = 16 * (((lane & 7) >> 1) ^ ((row >> 1) & 3)) + 8 * (lane & 1);  // (row + 16 has the same swizzle)
-              *reinterpret_cast<uint2*>(stage + row * 64 + at) = hi;
-              *reinterpret_cast<uint2*>(stage + (row + 16) * 64 + at) = lo;
-            } else {
-              *reinterpret_cast<uint4*>(smem + kPgQR + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(scale_bf16x2(x[k].x, inv[k]), scale_bf16x2(x[k].y, inv[k]), scale_bf16x2(x[k].z, inv[k]),
-                             scale_bf16x2(x[k].w, inv[k]));
-            }
+            *reinterpret_cast<uint4*>(smem + kPgQR + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+                make_uint4(scale_bf16x2(x[2 + k].x, inv[k]), scale_bf16x2(x[2 + k].y, inv[k]),
+                           scale_bf16x2(x[2 + k].z, inv[k]), scale_bf16x2(x[2 + k].w, inv[k]));
           }
-          if (i == 8) break;
-          named_bar_sync(1, 256);
-          uint4 c[2];
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQFull));
+
+        nt = walk.segment();
+        row = walk.t;
+        whole = nt == walk.ntiles;
+        head_part = walk.tile == 0;
+        walk.advance(nt);
+      }
+      // --- the first row's scale, or the next one's while the first scores are made: 2^-e with max |q| <= 448 2^e, eight
+      // heads a warp.  An infinite or NaN value (codes have no infinity) makes all of the head's codes NaN.
+      if (walk.left > 0) {
+        uint32_t amax[8];
+        const uint16_t* qw = q + ((long long)walk.t * 64 + 8 * sw) * 576;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            c[k] = *reinterpret_cast<const uint4*>(stage + own_row * 64 + 16 * ((2 * w2 + k) ^ ((own_row >> 1) & 3)));
-          tmem_st8(lane_addr + kPgQCol + 16 * i + 8 * w2, reinterpret_cast<const uint32_t*>(c));
-          named_bar_sync(1, 256);
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x0 = *reinterpret_cast<const uint4*>(qw + 576 * i + 8 * lane);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(qw + 576 * i + 256 + 8 * lane);
+          const uint32_t xr = *reinterpret_cast<const uint32_t*>(qw + 576 * i + 512 + 2 * lane);
+          amax[i] = __vmaxu2(__vmaxu2(max_abs_bf16(x0), max_abs_bf16(x1)), xr & 0x7fff7fffu);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t a = __reduce_max_sync(0xffffffffu, max(amax[i] << 16, amax[i] & 0xffff0000u));
+          const int e = max(int(a >> 23) - 135 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          if (lane == 0) qinv_s[8 * sw + i] = a < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
         }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarQFull));
-
-      const int nt = walk.segment();
-      row = walk.t;
-      whole = nt == walk.ntiles;
-      head_part = walk.tile == 0;
-      walk.advance(nt);
+      if (seg < 0) continue;
+      // --- the row's tiles
+      const f32x2 g2 = f2_pack(g, g);
       float off = 0.f, most = -INFINITY;  // kPgShift - m, and the x that asks for a new m
       m = -INFINITY;
       l2 = 0ull;
@@ -890,9 +901,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           mbar_arrive(bar(kBarRowEmpty + n % kPgRows));
           mbar_arrive(bar(kBarPFull));
         }
-        if (walk.left > 0 && scaled < 2) scale_heads(walk.t);
       }
-      ++seg;
     }
     if (!ok && st == 0) raise_status(kStatusTimeout);
   }
