@@ -852,6 +852,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (sw < 4 && part == 0) alpha_s[head] = al;
           resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
         }
+        // u = 2^x, rounded to fp16 for the value product; the sum takes it unrounded
+        uint32_t w[16];
+#pragma unroll
+        for (int i0 = 0; i0 < 16; i0 += 2) {
+          const ulonglong2 inv = *reinterpret_cast<const ulonglong2*>(cs_s + 256 + 2 * i0);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float a0, a1;
+            f2_unpack(x[i0 + e], a0, a1);
+            a0 = fast_exp2(a0);
+            a1 = fast_exp2(a1);
+            l2 = f2_fma(f2_pack(a0, a1), e ? inv.y : inv.x, l2);
+            const __half2 p = __floats2half2_rn(a0, a1);
+            w[i0 + e] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+        }
         // P and O are free once the previous value product is done
         if (t > 0 && !(ok = group_wait(bar(kBarPFree), uint32_t(n - 1) & 1u))) break;
         if (resc) {
@@ -873,27 +889,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           tmem_wait_st();
         }
-        // u = 2^x, rounded to fp16 for the value product; the sum takes it unrounded
         uint8_t* prow = smem + kPgP + part * 8192 + head * 128;
 #pragma unroll
-        for (int i0 = 0; i0 < 16; i0 += 4) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const ulonglong2 inv = *reinterpret_cast<const ulonglong2*>(cs_s + 256 + 2 * (i0 + i));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float a0, a1;
-              f2_unpack(x[i0 + i + e], a0, a1);
-              a0 = fast_exp2(a0);
-              a1 = fast_exp2(a1);
-              l2 = f2_fma(f2_pack(a0, a1), e ? inv.y : inv.x, l2);
-              const __half2 p = __floats2half2_rn(a0, a1);
-              w[i + e] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-          }
-          *reinterpret_cast<uint4*>(prow + (((4 * w2 + (i0 >> 2)) ^ (head & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(prow + (((4 * w2 + i) ^ (head & 7)) << 4)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -915,54 +915,75 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   }
 }
 
-// Rows split over CTAs: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  The row that CTA
-// blockIdx.x of the attention ended inside: its own partial result 1, then partial result 0 of the CTAs behind it.
-// Grid (attention CTAs, 8): eight heads a block, one per warp.
-__global__ void __launch_bounds__(256) paged_mla_merge_kernel(const int2* __restrict__ meta,
-                                                              const float* __restrict__ part,
-                                                              __nv_bfloat16* __restrict__ o_lat,
-                                                              float* __restrict__ lse) {
+// Rows split over CTAs: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  The row that CTA c of the
+// attention ended inside: its own partial result 1, then partial result 0 of the CTAs behind it.  Every block lists the
+// split rows; a warp takes 128 dims of one head of one of them at a time, with eight partial results in flight.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const int2* __restrict__ meta, int ctas,
+                                                                        const float* __restrict__ part,
+                                                                        __nv_bfloat16* __restrict__ o_lat,
+                                                                        float* __restrict__ lse) {
+  __shared__ int list[kPgMaxGrid], warp_count[kMergeThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int2 sp = meta[blockIdx.x];
-  if (sp.x < 0) return;
-  const int lane = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  auto at = [&](int i) {
-    return part + (long long)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * kPartFloats;
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < sp.y; i += 32) M = fmax_(M, at(i)[64 * 512 + h]);
+  static_assert(kPgMaxGrid <= kMergeThreads, "a thread looks at one CTA");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool split = int(threadIdx.x) < ctas && meta[threadIdx.x].x >= 0;
+  const uint32_t votes = __ballot_sync(0xffffffffu, split);
+  if (lane == 0) warp_count[warp] = __popc(votes);
+  __syncthreads();
+  int before = 0, rows = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmax_(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float M0 = M == -INFINITY ? 0.f : M;
-  float den = 0.f;
-  float4 acc[4];
+  for (int w = 0; w < kMergeThreads / 32; ++w) {
+    before += w < warp ? warp_count[w] : 0;
+    rows += warp_count[w];
+  }
+  if (split) list[before + __popc(votes & ((1u << lane) - 1u))] = threadIdx.x;
+  __syncthreads();
+  for (int u = blockIdx.x * (kMergeThreads / 32) + warp; u < rows * 256; u += gridDim.x * (kMergeThreads / 32)) {
+    const int cta = list[u >> 8], h = (u >> 2) & 63, d = 128 * (u & 3) + 4 * lane;
+    const int2 sp = meta[cta];  // row, parts
+    auto at = [&](int i) { return part + (long long)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kPartFloats; };
+    float M = -INFINITY;
+    for (int i = lane; i < sp.y; i += 32) M = fmaxf(M, at(i)[64 * 512 + h]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < sp.y; ++i) {
-    const float* p = at(i);
-    const float w = fast_exp2(p[64 * 512 + h] - M0);
-    den = fmaf(w, p[64 * 512 + 64 + h], den);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float M0 = M == -INFINITY ? 0.f : M;
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < sp.y; i0 += 32) {
+      // lane i holds the weight of part i0 + i (0 behind the last), so the parts' own loads need not wait for it
+      const bool has = i0 + lane < sp.y;
+      const float w = has ? fast_exp2(at(i0 + lane)[64 * 512 + h] - M0) : 0.f;
+      const float wl = has ? w * at(i0 + lane)[64 * 512 + 64 + h] : 0.f;
+      den += wl;
+      const int n = min(32, sp.y - i0);
+      for (int j = 0; j < n; j += 8) {
+        float4 x[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 x = *reinterpret_cast<const float4*>(p + h * 512 + 128 * k + 4 * lane);
-      acc[k].x = fmaf(w, x.x, acc[k].x);
-      acc[k].y = fmaf(w, x.y, acc[k].y);
-      acc[k].z = fmaf(w, x.z, acc[k].z);
-      acc[k].w = fmaf(w, x.w, acc[k].w);
+        for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4*>(at(i0 + min(j + k, n - 1)) + h * 512 + d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
+          if (j + k < n) {
+            acc.x = fmaf(wk, x[k].x, acc.x);
+            acc.y = fmaf(wk, x[k].y, acc.y);
+            acc.z = fmaf(wk, x[k].z, acc.z);
+            acc.w = fmaf(wk, x[k].w, acc.w);
+          }
+        }
+      }
     }
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  __nv_bfloat16* dst = o_lat + ((long long)sp.x * 64 + h) * 512;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
-    *reinterpret_cast<uint2*>(dst + 128 * k + 4 * lane) =
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(o_lat + ((long long)sp.x * 64 + h) * 512 + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if (lse && (u & 3) == 0 && lane == 0)
+      lse[(long long)sp.x * 64 + h] = den == 0.f ? -INFINITY : (M0 - kPgShift + log2f(den)) * 0.69314718055994531f;
   }
-  if (lse && lane == 0)
-    lse[(long long)sp.x * 64 + h] = den == 0.f ? -INFINITY : (M0 - kPgShift + log2f(den)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -995,7 +1016,10 @@ cudaError_t launch_paged_mla(const PagedMlaLaunch& p) {
                              kPgSmemAlloc, p.stream, 1, p.q, p.T, p.cu_q, p.seq_len, p.idx, p.topk, p.cache,
                              p.scale * 1.4426950408889634f, o, p.lse, meta, part, WaitLimit{p.wait_ns});
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_pdl(paged_mla_merge_kernel, dim3(grid, 8), dim3(256), 0, p.stream, 1, meta, part, o, p.lse);
+  // at most one split row per CTA, 32 blocks' worth of warps each
+  const unsigned blocks = grid * 32u < 4u * unsigned(p.sm_count) ? grid * 32u : 4u * unsigned(p.sm_count);
+  return launch_pdl(paged_mla_merge_kernel, dim3(blocks), dim3(kMergeThreads), 0, p.stream, 1, meta, int(grid), part, o,
+                    p.lse);
 }
 
 }  // namespace dsa
