@@ -77,8 +77,8 @@ __device__ __forceinline__ int row_exponent(uint32_t bits) {
 
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float(uint32_t(k + 127) << 23); }
 
-// One warp per row: lane l holds latent values 16 l .. 16 l + 15 and rope values
-// 2 l, 2 l + 1, so the row is read and written in whole lines.
+// One warp per row: lane l holds latent values 8 l .. 8 l + 7, 256 + 8 l .. + 7 and
+// rope values 2 l, 2 l + 1, so every load and store of the warp is whole lines.
 __global__ void __launch_bounds__(kCacheThreads)
     cache_write_kernel(const uint16_t* __restrict__ rows, long long rows_ld, int T, const int32_t* __restrict__ cu_q,
                        const int32_t* __restrict__ seq_len, PagedCache c) {
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int t = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   if (t >= T) return;
   const uint16_t* src = rows + t * rows_ld;
-  const uint4 x0 = *reinterpret_cast<const uint4*>(src + 16 * lane);
-  const uint4 x1 = *reinterpret_cast<const uint4*>(src + 16 * lane + 8);
+  const uint4 x0 = *reinterpret_cast<const uint4*>(src + 8 * lane);
+  const uint4 x1 = *reinterpret_cast<const uint4*>(src + 256 + 8 * lane);
   const uint32_t xr = *reinterpret_cast<const uint32_t*>(src + 512 + 2 * lane);
 
   const int b = owner_of(cu_q, c.batch, t);
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kCacheThreads)
     code[i] = lo | (hi << 16);
   }
   uint8_t* dst = c.kv8 + (long long)row * kRow8;
-  *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(code[0], code[1], code[2], code[3]);
+  *reinterpret_cast<uint2*>(dst + 8 * lane) = make_uint2(code[0], code[1]);
+  *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = make_uint2(code[2], code[3]);
   const __nv_bfloat162 r2 =
       __floats2bfloat162_rn(__uint_as_float(xr << 16) * inv, __uint_as_float(xr & 0xffff0000u) * inv);
   *reinterpret_cast<__nv_bfloat162*>(dst + 512 + 4 * lane) = r2;
@@ -210,21 +211,15 @@ __global__ void __launch_bounds__(kCacheThreads)
     const int row = cache_row(c, b, int(s));
     if (row < 0) continue;
     const uint8_t* src = c.kv8 + (long long)row * kRow8;
-    const uint4 q = *reinterpret_cast<const uint4*>(src + 16 * lane);
+    const uint2 q0 = *reinterpret_cast<const uint2*>(src + 8 * lane);
+    const uint2 q1 = *reinterpret_cast<const uint2*>(src + 256 + 8 * lane);
     const __nv_bfloat162 r = *reinterpret_cast<const __nv_bfloat162*>(src + 512 + 4 * lane);
     const float f = c.kv_scale[row];
     uint16_t* dst = kv + (kv_start[b] + s) * 576;
-    uint4 o0, o1;
-    o0.x = codes_to_bf16x2(q.x, f);
-    o0.y = codes_to_bf16x2(q.x >> 16, f);
-    o0.z = codes_to_bf16x2(q.y, f);
-    o0.w = codes_to_bf16x2(q.y >> 16, f);
-    o1.x = codes_to_bf16x2(q.z, f);
-    o1.y = codes_to_bf16x2(q.z >> 16, f);
-    o1.z = codes_to_bf16x2(q.w, f);
-    o1.w = codes_to_bf16x2(q.w >> 16, f);
-    *reinterpret_cast<uint4*>(dst + 16 * lane) = o0;
-    *reinterpret_cast<uint4*>(dst + 16 * lane + 8) = o1;
+    *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(codes_to_bf16x2(q0.x, f), codes_to_bf16x2(q0.x >> 16, f),
+                                                           codes_to_bf16x2(q0.y, f), codes_to_bf16x2(q0.y >> 16, f));
+    *reinterpret_cast<uint4*>(dst + 256 + 8 * lane) = make_uint4(codes_to_bf16x2(q1.x, f), codes_to_bf16x2(q1.x >> 16, f),
+                                                                 codes_to_bf16x2(q1.y, f), codes_to_bf16x2(q1.y >> 16, f));
     *reinterpret_cast<__nv_bfloat162*>(dst + 512 + 2 * lane) =
         __floats2bfloat162_rn(__low2float(r) * f, __high2float(r) * f);
   }
