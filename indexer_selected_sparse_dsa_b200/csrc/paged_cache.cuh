@@ -61,7 +61,7 @@ __device__ __forceinline__ int seen_by(const PagedCache& c, const int32_t* __res
                                        const int32_t* __restrict__ seq_len, int b, int t) {
   const int q0 = cu_q[b], q1 = cu_q[b + 1], len = seq_len[b];
   const long long seen = (long long)len - ((long long)q1 - t) + 1;
-  if (t < q0 || t >= q1 || seen < 1 || len > max_positions(c)) {
+  if (q0 < 0 || t < q0 || t >= q1 || seen < 1 || len > max_positions(c)) {
     raise_status(kStatusBadRow);
     return 0;
   }

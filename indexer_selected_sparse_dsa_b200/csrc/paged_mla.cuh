@@ -84,6 +84,16 @@ constexpr int kPgSmem = kPgTailOff + 64;
 constexpr int kPgSmemAlloc = kPgSmem + 1024;
 constexpr uint32_t kPgQCol = 128, kPgOCol = 256;             // S: 128 columns; Q: 128 (512 codes); O^T: 4 x 64
 
+// ln(2^(m - kPgShift) l), -inf for l = 0.  m and l may be far from 1 in opposite directions (by a row's 2^k): whole
+// exponents are added first, so that the sum is rounded at its own size.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  const uint32_t bits = __float_as_uint(l);
+  if (l == 0.f) return -INFINITY;
+  if (bits - 0x00800000u >= 0x7f000000u) return (m - kPgShift + log2f(l)) * 0.69314718055994531f;  // not a normal number
+  const float e = float(int(bits >> 23) - 127), f = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
+  return ((m - kPgShift + e) + log2f(f)) * 0.69314718055994531f;
+}
+
 // Query rows of sequence b: 0 (and the status bit) where cu_q is not in order.
 __device__ __forceinline__ int seq_rows(const int32_t* __restrict__ cu_q, int T, int b, int& q0, bool report) {
   q0 = cu_q[b];
@@ -696,7 +706,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               prow[head] = m;
               prow[64 + head] = l;
             } else if (lse) {
-              lse[(long long)row * 64 + head] = l == 0.f ? -INFINITY : (m - kPgShift + log2f(l)) * 0.69314718055994531f;
+              lse[(long long)row * 64 + head] = log_sum(m, l);
             }
           }
           __syncwarp();
@@ -982,7 +992,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
     *reinterpret_cast<uint2*>(o_lat + ((long long)sp.x * 64 + h) * 512 + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     if (lse && (u & 3) == 0 && lane == 0)
-      lse[(long long)sp.x * 64 + h] = den == 0.f ? -INFINITY : (M0 - kPgShift + log2f(den)) * 0.69314718055994531f;
+      lse[(long long)sp.x * 64 + h] = log_sum(M0, den);
   }
 }
 

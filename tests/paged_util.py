@@ -111,7 +111,7 @@ class Batch:
             seq, sc = self.values(b, m), self.scales(b, m)
             for j in range(n):
                 t = int(self.cu[b]) + j
-                seen = m - n + j + 1
+                seen = max(m - n + j + 1, 0)
                 k, ks = seq[:seen], sc[:seen]
                 if idx is not None:
                     s = torch.as_tensor(idx[t]).long().cuda()
