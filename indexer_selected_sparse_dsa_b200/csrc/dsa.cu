@@ -328,6 +328,15 @@ int check_paged(const int32_t* cu_q, const int32_t* seq_len, const int32_t* page
   return DSA_OK;
 }
 
+dsa::PagedCache paged_cache(const uint8_t* kv8, const float* kv_scale, const int32_t* page_table, int batch,
+                            int max_pages, int n_pages, int page_size) {
+  int l = 0;
+  while ((int64_t(1) << l) < page_size) ++l;
+  const uint64_t mul = ((uint64_t(1) << (31 + l)) + page_size - 1) / page_size;
+  return {const_cast<uint8_t*>(kv8), const_cast<float*>(kv_scale), page_table, batch, max_pages, n_pages, page_size,
+          uint32_t(mul), 31 + l};
+}
+
 // max_keys: the keys a query row can have (its selection, or the longest sequence)
 size_t ws_paged_mla(int T, int64_t max_keys) {
   return T > 0 && max_keys > 0 ? align_up(dsa::paged_mla_ws_bytes(T, max_keys), 256) : 0;
@@ -360,7 +369,7 @@ int run_paged_mla(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* 
   p.seq_len = seq_len;
   p.idx = idx;
   p.topk = topk;
-  p.cache = {const_cast<uint8_t*>(kv8), const_cast<float*>(kv_scale), page_table, batch, max_pages, n_pages, page_size};
+  p.cache = paged_cache(kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size);
   p.scale = scale;
   p.o_lat = o_lat;
   p.lse = lse;
@@ -807,7 +816,7 @@ int dsa_cache_write(const dsa_bf16* rows, int64_t rows_ld, int T, const int32_t*
   DeviceState* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   dsa::CacheWriteLaunch p{rows, rows_ld, T, cu_q, seq_len,
-                          {kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size}, stream};
+                          paged_cache(kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size), stream};
   cudaError_t e = dsa::launch_cache_write(p);
   if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
   return DSA_OK;
@@ -825,8 +834,7 @@ int dsa_cache_read(const uint8_t* kv8, const float* kv_scale, int n_pages, int p
   if (!aligned(kv, 16)) return fail(DSA_ERR_INVALID_ARG, "kv must be 16-byte aligned");
   DeviceState* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
-  dsa::CacheReadLaunch p{{const_cast<uint8_t*>(kv8), const_cast<float*>(kv_scale), page_table, batch, max_pages, n_pages,
-                          page_size}, seq_len, kv_start, kv, cache_rows, dev->sm_count, stream};
+  dsa::CacheReadLaunch p{paged_cache(kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size), seq_len, kv_start, kv, cache_rows, dev->sm_count, stream};
   cudaError_t e = dsa::launch_cache_read(p);
   if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
   return DSA_OK;

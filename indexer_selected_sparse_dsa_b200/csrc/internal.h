@@ -132,6 +132,11 @@ struct PagedCache {
   int max_pages;
   int n_pages;
   int page_size;
+  // s / page_size = s * page_mul >> page_shift for 0 <= s < 2^31: with l = ceil(log2 page_size), page_shift = 31 + l
+  // and page_mul = ceil(2^page_shift / page_size), which exceeds the quotient by less than page_size / page_size
+  // <= 2^l / page_size, too little to matter below 2^31.
+  uint32_t page_mul;
+  int page_shift;
 };
 struct CacheWriteLaunch {
   const uint16_t* rows;

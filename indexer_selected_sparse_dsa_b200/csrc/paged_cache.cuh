@@ -24,10 +24,15 @@ constexpr int kRow8 = 640;       // bytes of a cache row: 512 codes, 64 bf16
 constexpr int kExpMin = -60, kExpMax = 60;
 constexpr int kCacheThreads = 256;
 
+// The page of its sequence that position s lies in (an integer division takes some 20 instructions).
+__device__ __forceinline__ int page_index(const PagedCache& c, int s) {
+  return int((unsigned long long)unsigned(s) * c.page_mul >> c.page_shift);
+}
+
 // The row of the flattened cache that holds position s of sequence b, or -1
 // (and the status bit) where the page table points outside the cache.
 __device__ __forceinline__ int cache_row(const PagedCache& c, int b, int s) {
-  const int p = int(unsigned(s) / unsigned(c.page_size));
+  const int p = page_index(c, s);
   const int page = c.page_table[(long long)b * c.max_pages + p];
   if (page < 0 || page >= c.n_pages) {
     raise_status(kStatusBadRow);

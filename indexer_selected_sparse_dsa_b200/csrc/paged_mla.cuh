@@ -294,11 +294,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kPgThreads / 32; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+    long long all = lane < kPgThreads / 32 ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += up;
     }
+    const long long total = __shfl_sync(0xffffffffu, all, 31);
+    const long long before = warp > 0 ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
     const long long share = (total + gridDim.x - 1) / gridDim.x;
     const long long g0 = share * blockIdx.x, g1 = min(g0 + share, total);
     long long at = before + incl - mine;
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // that follow from each other; each is made one tile after the one before it,
     // so that none is waited for.
     const int total = walk.left;
-    int s2[4], s1[4], page1[4], row0[4], b2;
+    int s2[4], s1[4], page1[4], row0[4], b2, seen2 = 0;
     float sc0[4];
     int seen_row = -1;
     auto position = [&]() {  // of the walk's next tile (-1: none); then step on
@@ -405,22 +408,23 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (!kSparse) {
             s = j < walk.seen ? j : -1;
           } else if (j < topk) {
-            s = idx[(long long)walk.t * topk + j];
-            if (s >= walk.seen) {
-              raise_status(kStatusBadRow);
-              s = -1;
-            }
+            s = idx[(long long)walk.t * topk + j];  // (looked at a step later)
           }
         }
         s2[i] = s;
       }
+      seen2 = walk.seen;
       if (walk.left > 0) walk.advance(1);
     };
     auto page = [&]() {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (kSparse && s2[i] >= seen2) {
+          raise_status(kStatusBadRow);
+          s2[i] = -1;
+        }
         s1[i] = s2[i];
-        page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + int(unsigned(s2[i]) / unsigned(c.page_size))] : 0;
+        page1[i] = s2[i] >= 0 ? c.page_table[(long long)b2 * c.max_pages + page_index(c, s2[i])] : 0;
       }
     };
     auto scale = [&]() {
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       for (int i = 0; i < 4; ++i) {
         int y = -1;
         if (s1[i] >= 0) {
-          if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + int(unsigned(s1[i]) % unsigned(c.page_size));
+          if (page1[i] >= 0 && page1[i] < c.n_pages) y = page1[i] * c.page_size + (s1[i] - page_index(c, s1[i]) * c.page_size);
           else raise_status(kStatusBadRow);
         }
         row0[i] = y;
