@@ -9,8 +9,8 @@
 // q = 2^e (hi + lo / 16), both e4m3 (4 + 4 significant bits: exact for values
 // within 2^5 of the head's largest, never off by more than 2^-22 of it), so
 // the 8-bit tensor path multiplies the cache's codes as they lie in memory:
-// N = 128 columns, 64 of hi and 64 of lo.  The rope half follows in bf16 into
-// the hi columns.  2^k_s, 2^e and the scale are applied to the fp32 sums.
+// M = 128 rows, 64 of hi and 64 of lo.  The rope half follows in bf16 on top of
+// the hi rows.  2^k_s, 2^e and the scale are applied to the fp32 sums.
 //
 // Values as fp16.  A code is exact in fp16, and a probability rounded to fp16
 // (2^-11) is eight times closer than one in bf16.  The row's 2^k goes into the
@@ -24,8 +24,17 @@
 // codes), the keys are the B operand, and S comes out with a lane per head.  One
 // 16x32bx2 load then hands a thread the hi sums of its head, another the lo sums
 // of the same keys: maximum, sum and scale of a head are registers, not a reduction
-// over threads.  What is left in shared memory a tile: the codes once in (80 KB),
-// once out, the widened values in (128 KB) and out, and P.
+// over threads.
+//
+// What bounds it: per 128-key tile the tensor pipe works 1024 (codes) + 260 (rope)
+// + 1600 (values; M = 128, N = 64 takes 50 cycles a step, the operands' reads from
+// shared memory) = 2900 cycles, and shared memory moves 80 KB of codes in and 96 KB
+// of operands out for S, 128 KB of widened values in and 192 KB out for O, 16 KB of
+// P: some 4300 cycles at 128 bytes each, against 3500 that a tile's 82 KB take from
+// HBM.  Measured 5400 cycles a tile, 11000 more where a CTA goes on to another query
+// row.  64 sequences of 2K to 16K positions, one token: 137 us (3.1 TB/s, 0.47 of
+// the measured copy rate); 512 tokens over 8192 positions: 0.79 ms (820 TFLOP/s,
+// 0.51 of the measured bf16 rate); 64 x 2048 selected rows: 53 us.
 //
 // One CTA walks an equal share of all 128-key tiles of the batch, query row
 // after query row; a row that ends in another CTA leaves partial sums that
@@ -336,8 +345,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   else if (threadIdx.x == 0) meta[blockIdx.x] = make_int2(-1, 0);
 
   // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back in some 10 ns, so the
-  // limit is counted in tries: the code of 18 waits has to stay short (see the issuing warp).  Who gives up leaves its
-  // loop; the roles that wait for it run into their own limits.
+  // limit is counted in tries: five warps of four roles share a scheduler's instruction cache, and the code of 18 waits
+  // has to stay short (with the clock read in each, and loops unrolled, a tile took 7100 cycles).  Who gives up leaves
+  // its loop; the roles that wait for it run into their own limits.
   const uint32_t tries = uint32_t(min(lim.ns / 10, 2000000000ull)) + 1;
   auto warp_wait = [&](uint32_t b, uint32_t parity) {
     uint32_t left = tries;
@@ -845,6 +855,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarSFree));
+        if (reinterpret_cast<const int*>(keys_of(n))[0] < 0) {  // no key in the tile: whatever the query holds
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = f2_pack(-INFINITY, -INFINITY);
+          top = -INFINITY;
+        }
         int resc = 0;
         if (bar_red_or(1, 256, top > most)) {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));

@@ -312,6 +312,20 @@ def test_a_nonfinite_query_value_stays_in_its_head(bad, dim):
 
 
 @pytest.mark.gpu
+def test_rows_that_see_nothing_ignore_their_query():
+    """An all-empty selection gives 0 and -inf, NaN queries or not; so does one empty tile beside a full one."""
+    c = Batch([2, 1], [400, 300], 16, seed=19)
+    idx = selection(c, 256, seed=20)
+    idx[0] = -1
+    idx[2, :128] = -1
+    c.q[0] = float("nan")
+    o, lse = run_selected(c, idx)
+    B.dsa_sync_status()
+    c.q[0] = 0
+    check_attention(c, o, lse, idx)
+
+
+@pytest.mark.gpu
 def test_large_and_small_queries():
     """Heads of one row whose queries differ by many powers of two, and an all-zero one (the mean of the values)."""
     import torch
