@@ -297,7 +297,8 @@ DSA_API int dsa_indexer_scores_noalloc(const dsa_bf16* q_I, const dsa_bf16* w, c
  * Its new tokens are the query rows cu_q[b] .. cu_q[b+1]-1 (any number, also
  * none) and the last of its seq_len[b] positions: row t stands at position
  * seq_len[b] - (cu_q[b+1] - t) and sees the positions up to its own.  Query
- * rows from cu_q[batch] on belong to no sequence and are left alone.
+ * rows before cu_q[0] and from cu_q[batch] on belong to no sequence and are left
+ * alone.  Sequences may share pages that only are read.
  *
  *  T           rows of the row tensors, at least cu_q[batch]
  *  cu_q        [batch+1] int32 (device), not decreasing
@@ -308,7 +309,10 @@ DSA_API int dsa_indexer_scores_noalloc(const dsa_bf16* q_I, const dsa_bf16* w, c
  *              any page_size >= 1, n_pages * page_size <= 2^31-1
  * A query row whose numbers do not fit together, or a page outside the cache,
  * sets the status bit (dsa_sync_status: DSA_ERR_BAD_ROW); what each entry point
- * then does with the row stands below.
+ * then does with the row stands below.  Where cu_q itself decreases or passes T,
+ * nothing is read or written out of range, and the rows between are undefined.
+ * kv_scale of a row that is read must be a power of two in [2^-60, 2^60], as
+ * dsa_cache_write stores it.
  */
 
 /*
@@ -329,7 +333,8 @@ DSA_API int dsa_cache_write(const dsa_bf16* rows, int64_t rows_ld, int T, const 
  *     kv[kv_start[b] + s, :] = 2^k (codes || rope)   in bf16,
  * the layout that dsa_forward, dsa_sparse_mla_attn and the others read.  Other
  * rows of kv are left as they were; so are those of a sequence whose seq_len or
- * kv_start does not fit (status bit), and those in a page outside the cache.
+ * kv_start does not fit (status bit), and those in a page outside the cache.  Two
+ * sequences that claim the same flat row leave it undefined.
  *
  *  kv_start [batch] int64 (device); kv [cache_rows,576] bf16, 16-byte aligned
  */
@@ -348,7 +353,8 @@ DSA_API int dsa_cache_read(const uint8_t* kv8, const float* kv_scale, int n_page
  *  o_lat  [T,64,512] bf16, 16-byte aligned (bf16 here: what follows is a product
  *         with bf16 weights); lse [T,64] fp32 or NULL
  *  ws     >= dsa_workspace_size(DSA_OP_PAGED_MLA, T, max_pages * page_size, 0) bytes,
- *         256-byte aligned: partial results of rows that are split over CTAs
+ *         256-byte aligned: partial results of rows that are split over CTAs; calls
+ *         that may run at the same time need one each, calls on one stream can share it
  * A row that sees nothing, or whose numbers do not fit (status bit), gets
  * o_lat = 0 and lse = -inf; a position in a page outside the cache is skipped
  * (status bit).
@@ -362,8 +368,9 @@ DSA_API int dsa_paged_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, co
  * The same over each row's selected positions, as dsa_topk and dsa_indexer_topk
  * write them: dsa_sparse_mla_attn over the paged 8-bit cache.
  *
- *  idx  [T,topk] int32, 1 <= topk <= 2048: positions in the row's sequence, -1 =
- *       empty slot; an entry at or beyond what the row sees is skipped (status bit)
+ *  idx  [T,topk] int32, 1 <= topk <= 2048: positions in the row's sequence in any
+ *       order, negative = empty slot, anywhere; an entry at or beyond what the row
+ *       sees is skipped (status bit); a position named twice counts twice
  *  ws   >= dsa_workspace_size(DSA_OP_PAGED_MLA, T, max_pages * page_size, topk) bytes, 256-byte aligned
  */
 DSA_API int dsa_paged_sparse_mla_attn(const dsa_bf16* q, int T, const int32_t* cu_q, const int32_t* seq_len,

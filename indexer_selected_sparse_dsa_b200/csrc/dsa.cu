@@ -834,7 +834,8 @@ int dsa_cache_read(const uint8_t* kv8, const float* kv_scale, int n_pages, int p
   if (!aligned(kv, 16)) return fail(DSA_ERR_INVALID_ARG, "kv must be 16-byte aligned");
   DeviceState* dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
-  dsa::CacheReadLaunch p{paged_cache(kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size), seq_len, kv_start, kv, cache_rows, dev->sm_count, stream};
+  dsa::CacheReadLaunch p{paged_cache(kv8, kv_scale, page_table, batch, max_pages, n_pages, page_size),
+                         seq_len, kv_start, kv, cache_rows, dev->sm_count, stream};
   cudaError_t e = dsa::launch_cache_read(p);
   if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
   return DSA_OK;

@@ -132,9 +132,9 @@ struct PagedCache {
   int max_pages;
   int n_pages;
   int page_size;
-  // s / page_size = s * page_mul >> page_shift for 0 <= s < 2^31: with l = ceil(log2 page_size), page_shift = 31 + l
-  // and page_mul = ceil(2^page_shift / page_size), which exceeds the quotient by less than page_size / page_size
-  // <= 2^l / page_size, too little to matter below 2^31.
+  // s / page_size = s * page_mul >> page_shift for 0 <= s < 2^31: with l = ceil(log2 page_size), page_shift = 31 + l and
+  // page_mul = ceil(2^page_shift / page_size).  Rounding up adds less than s / 2^page_shift < 2^-l <= 1 / page_size to the
+  // quotient, too little to reach the next whole number; page_mul is below 2^32 since 2^l < 2 page_size.
   uint32_t page_mul;
   int page_shift;
 };

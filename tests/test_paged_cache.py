@@ -338,6 +338,53 @@ def test_large_and_small_queries():
     check_attention(c, o, lse)
 
 
+@pytest.mark.gpu
+def test_a_position_selected_twice_counts_twice():
+    c = Batch([1, 2], [300, 90], 16, seed=21)
+    idx = selection(c, 200, seed=22)
+    idx[0, 100:110] = idx[0, 3]
+    idx[2, 50:] = idx[2, 49]
+    o, lse = run_selected(c, idx)
+    B.dsa_sync_status()
+    check_attention(c, o, lse, idx)
+
+
+@pytest.mark.gpu
+def test_sequences_may_share_pages():
+    """A common prefix of four pages, read by both sequences."""
+    import torch
+    c = Batch([2, 1], [400, 300], 64, seed=23)
+    c.table[1, :4] = c.table[0, :4]
+    c.page_table = torch.from_numpy(c.table).cuda()
+    o, lse = run_dense(c)
+    B.dsa_sync_status()
+    check_attention(c, o, lse)
+
+
+@pytest.mark.gpu
+def test_query_rows_before_the_first_sequence():
+    """cu_q may begin behind row 0: the rows before it belong to no sequence."""
+    import torch
+    c = Batch([1, 2], [40, 50], 16, seed=24)
+    want = run_dense(c)
+    front = torch.full_like(c.q[:2], 3.0)
+    c.q, c.cu_q, c.T = torch.cat([front, c.q]), c.cu_q + 2, c.T + 2
+    o, lse = run_dense(c)
+    B.dsa_sync_status()
+    assert bool((o[:2] == 7.0).all()) and bool((lse[:2] == 7.0).all())
+    c.q = c.q[2:]
+    check_attention(c, o[2:], lse[2:])
+    check_attention(c, *want)
+    before = c.kv8.clone(), c.kv_scale.clone()
+    at = torch.from_numpy(np.concatenate([c.slots(0, [39]), c.slots(1, [48, 49])])).cuda()
+    c.kv8.view(-1, ROW8)[at] = 0
+    c.kv_scale.view(-1)[at] = 0
+    rows = torch.cat([torch.full((2, ROW), 9.0, dtype=torch.bfloat16, device="cuda"), c.rows[at]])
+    B.dsa_cache_write(rows, *c.plan, c.kv8, c.kv_scale)
+    B.dsa_sync_status()
+    assert torch.equal(c.kv8, before[0]) and torch.equal(c.kv_scale, before[1])
+
+
 # ------------------------------------------------------------------ rows and pages that do not fit
 
 def bad_status(fn):
