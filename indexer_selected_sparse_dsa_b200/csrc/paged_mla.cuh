@@ -89,7 +89,7 @@ enum PgBar {
   kBarVEmpty = kBarVFull + kPgVSlots, kBarRowFull = kBarVEmpty + kPgVSlots, kBarRowEmpty = kBarRowFull + kPgRows,
   kPgBars = kBarRowEmpty + kPgRows
 };
-constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, start (b, t, tile), tiles before start and end
+constexpr int kPgTailOff = kPgBarOff + 8 * kPgBars;          // tmem address, start (b, t, tile), share, tiles before start and end
 constexpr int kPgSmem = kPgTailOff + 64;
 constexpr int kPgSmemAlloc = kPgSmem + 1024;
 constexpr uint32_t kPgQCol = 128, kPgOCol = 256;             // S: 128 columns; Q: 128 (512 codes); O^T: 4 x 64
@@ -202,6 +202,12 @@ __device__ __forceinline__ void store_fp16(uint8_t* s0, uint8_t* s1, const uint4
 __device__ __forceinline__ uint32_t max_abs_bf16(const uint4& x) {
   return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 }
+// 2^-e with max |q| <= 448 2^e, from the largest magnitude's fp32 pattern.  NaN where that is infinite or NaN (codes have
+// no infinity): all of the head's codes become NaN.
+__device__ __forceinline__ float query_scale(uint32_t a) {
+  const int e = max(int(a >> 23) - 135 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+  return a < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
+}
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, f32x2 inv) {
   float a, b;
   f2_unpack(f2_mul(f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), inv), a, b);
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   float* linv_s = alpha_s + 64;
   float* qinv_s = alpha_s + 128;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPgTailOff);
-  int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile where this CTA begins
+  int* start_s = reinterpret_cast<int*>(smem + kPgTailOff + 8);  // b, t, tile where this CTA begins; a share
   long long* ends_s = reinterpret_cast<long long*>(smem + kPgTailOff + 24);  // the batch's tiles before it, and before the next
   // (by a shuffle, so that the compiler knows it to be the same in all lanes: the roles' addresses and descriptors
   // then live in uniform registers)
@@ -286,7 +292,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   // in its share of the line.  Against equal shares of tiles alone: 16 sequences of four drafted tokens 69 -> 62 us, 64 x
   // 2048 selected rows 52.5 -> 49.6 us, 300 positions 16.6 -> 17.2 us (two sums to scan).  A cost of 1 or 3 tiles: 64 and
   // 62 us, 52 and 51 us.
-  long long share;
   {
     longlong2* sums = reinterpret_cast<longlong2*>(smem);  // the warps' sums, in the rope half's room
     const int per = (c.batch + kPgThreads - 1) / kPgThreads;
@@ -322,7 +327,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int wb = max(warp - 1, 0);
     const longlong2 before = make_longlong2(__shfl_sync(0xffffffffu, all.x, wb), __shfl_sync(0xffffffffu, all.y, wb));
     const long long cost = all_tiles > gridDim.x ? kPgRowCost : 0;  // (at most one tile each: nothing to balance)
-    share = (all_tiles + cost * all_rows + gridDim.x - 1) / gridDim.x;
+    const long long share = (all_tiles + cost * all_rows + gridDim.x - 1) / gridDim.x;
+    if (threadIdx.x == 64) start_s[3] = int(min(share, 1ll << 30));  // (a row has less than 2^24 tiles)
     const long long x0 = incl.x - mine.x + (warp ? before.x : 0), y0 = incl.y - mine.y + (warp ? before.y : 0);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {  // where the share begins, and where it ends
@@ -365,18 +371,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   if (busy) walk.start(start_s, own_tiles);
   else if (threadIdx.x == 0) meta[blockIdx.x] = make_int2(-1, 0);
 
-  // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back in some 10 ns, so the
-  // limit is counted in tries: five warps of four roles share a scheduler's instruction cache, and the code of 18 waits
-  // has to stay short (with the clock read in each, and loops unrolled, a tile took 7100 cycles).  Who gives up leaves
-  // its loop; the roles that wait for it run into their own limits.
-  const uint32_t tries = uint32_t(min(lim.ns / 10, 2000000000ull)) + 1;
+  // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back after 4 us (measured), so
+  // the limit is counted in tries, and one shorter than a try gives up at once: five warps of four roles share a
+  // scheduler's instruction cache, and the code of 18 waits has to stay short (with the clock read in each, and loops
+  // unrolled, a tile took 7100 cycles).  Who gives up leaves its loop; the roles that wait for it run into their own limits.
+  const uint32_t tries = uint32_t(min(lim.ns / 4000, 1000000000ull)) + 1;
   auto warp_wait = [&](uint32_t b, uint32_t parity) {
     uint32_t left = tries;
     bool done;
 #pragma unroll 1
     do done = __all_sync(0xffffffffu, mbar_try_wait(b, parity)) != 0;
     while (!done && --left);
-    return done;
+    return done && tries > 1;
   };
   // The same for the softmax: one warp tries, and a barrier hands all 256 threads the outcome, so that they leave
   // together if they have to.
@@ -384,6 +390,57 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const bool done = warp == kPgSoft ? warp_wait(b, parity) : true;
     return bar_red_or(1, 256, done ? 0 : 1) == 0;
   };
+  // --- the first row's query, by the value and softmax warps together: eight lanes to a head keep it in registers, and its
+  // codes go through the room of the value slots in one step, where a later row's (below) go in eight through a small one
+  // (one row over 300 positions: 17.4 -> 15.3 us against the softmax warps alone by that way).
+  if (busy && warp >= kPgVWarp) {
+    const int l8 = lane & 7, h = 4 * (warp - kPgVWarp) + (lane >> 3), row = 32 * (h >> 4) + (h & 15);
+    const uint4* src = reinterpret_cast<const uint4*>(q + ((long long)walk.t * 64 + h) * 576) + l8;
+    uint4 x[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) x[i] = src[8 * i];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) a = __vmaxu2(a, max_abs_bf16(x[i]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float inv1 = query_scale(max(a << 16, a & 0xffff0000u));
+    if (l8 == 0) qinv_s[h] = inv1;
+    const f32x2 inv = f2_pack(inv1, inv1);
+    // 16-byte units of a row of 512 bytes: two neighbouring rows in different halves of 128 bytes, eight all apart
+    uint8_t* stage = smem + kPgV;
+    auto unit = [](int r, int u) { return r * 512 + ((u ^ (4 * (r & 1) + ((r >> 1) & 3))) << 4); };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint2 hi, lo;
+      split_codes(x[i].x, x[i].y, inv, hi.x, lo.x);
+      split_codes(x[i].z, x[i].w, inv, hi.y, lo.y);
+      uint8_t* to = stage + unit(row, 4 * i + (l8 >> 1)) + 8 * (l8 & 1);  // (the swizzle is the same 16 rows on)
+      *reinterpret_cast<uint2*>(to) = hi;
+      *reinterpret_cast<uint2*>(to + 16 * 512) = lo;
+    }
+    uint8_t* rope = smem + kPgQR + row * 128 + ((l8 ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(rope) = make_uint4(scale_bf16x2(x[8].x, inv), scale_bf16x2(x[8].y, inv),
+                                                 scale_bf16x2(x[8].z, inv), scale_bf16x2(x[8].w, inv));
+    *reinterpret_cast<uint4*>(rope + 16 * 128) = make_uint4(0, 0, 0, 0);  // the lo rows of the rope half stay zero
+    named_bar_sync(2, 512);
+    const int own = 32 * (warp & 3) + lane, piece = (warp >> 2) - 1;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float w[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(stage + unit(own, 8 * piece + 4 * j + k));
+        w[4 * k] = y.x, w[4 * k + 1] = y.y, w[4 * k + 2] = y.z, w[4 * k + 3] = y.w;
+      }
+      tmem_st16(tmem + (uint32_t(32 * (warp & 3)) << 16) + kPgQCol + 32 * piece + 16 * j, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    fence_proxy_async_smem();
+    named_bar_sync(2, 512);
+    if (warp >= kPgSoft && lane == 0) mbar_arrive(bar(kBarQFull));
+  }
   if (!busy) {
     // nothing to do
   } else if (warp < kPgMma) {
@@ -423,7 +480,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int total = walk.left;
     int s2[4], s1[4], page1[4], row0[4], b2, seen2 = 0;
     float sc0[4];
-    int seen_row = -1;
+    int seen_row = walk.t;  // (the first row's query is being read already)
     auto position = [&]() {  // of the walk's next tile (-1: none); then step on
       b2 = walk.b;
       if (walk.left > 0 && walk.t != seen_row) {  // a new row: its query is wanted soon
@@ -607,7 +664,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     uint8_t* const dst = smem + kPgV + voff;
     const int total = walk.left;
     int seg = 0, i = 0;  // rows begun, half tiles (256 dims) done
-    int2 split = make_int2(-1, 0);
+    if (vt == 0) meta[blockIdx.x] = make_int2(-1, 0);
     bool ok = true, any = false;
     const uint8_t* src[4];
     auto rows = [&](int n) {
@@ -647,8 +704,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       const int nt = walk.segment(), row = walk.t, tile = walk.tile;
       const bool whole = nt == walk.ntiles;
       if (!whole && tile == 0) {
-        const int rest = walk.ntiles - nt;
-        split = make_int2(row, 1 + int((rest + share - 1) / share));
+        const int rest = walk.ntiles - nt, share = start_s[3];
+        if (vt == 0) meta[blockIdx.x] = make_int2(row, 1 + (rest + share - 1) / share);
       }
       walk.advance(nt);
       const int end = i + 2 * nt;
@@ -696,7 +753,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarOFree));
       ++seg;
     }
-    if (vt == 0) meta[blockIdx.x] = ok ? split : make_int2(-1, 0);
+    if (!ok && vt == 0) meta[blockIdx.x] = make_int2(-1, 0);
     if (!ok && lane == 0) raise_status(kStatusTimeout);
   } else {
     // ---------------------------------------------------------------- softmax and queries
@@ -710,44 +767,40 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     float* red = reinterpret_cast<float*>(smem + kPgRedOff);
     bool ok = true;
 
-    // the lo rows of the rope half stay zero
-    for (int i = st; i < 64 * 8; i += 256)
-      *reinterpret_cast<uint4*>(smem + kPgQR + (32 * (i >> 7) + 16 + ((i >> 3) & 15)) * 128 + (i & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
-    int n = 0, seg = -1, nt = 0;  // tiles done, rows begun before this one
-    float g = 1.f;                // 2^e of the head's query
+    int n = 0, seg = 0, nt = 0;  // tiles done, rows begun before this one
+    float g = qinv_s[head];           // 2^e of the head's query
     // the head's running maximum m of y (a whole number) and sum (two keys side by side); the row they are of
     float m = -INFINITY;
     f32x2 l2 = 0ull;
     int row = 0;
     bool whole = false, head_part = false;
+    g = g == g ? 1.f / g : 1.f;
+    named_bar_sync(1, 256);  // (the next row's scale goes to the same place)
     for (;; ++seg) {  // (`ok` is the same in all threads of the role)
       const bool more = walk.left > 0;
-      if (seg >= 0) {
+      if (seg > 0) {
         // --- the sum of the row before: its reciprocal for the value role, which writes the result
-        if (seg > 0) {
-          if (!ok || (seg > 1 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg) & 1u)))) break;
-          float l, l1;
-          f2_unpack(l2, l, l1);
-          l += l1;
-          l += __shfl_xor_sync(0xffffffffu, l, 16);
-          if (part == 0) red[64 * w2 + head] = l;
-          named_bar_sync(1, 256);
-          if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
-            l = red[head] + red[64 + head];
-            linv_s[head] = l == 0.f ? 0.f : 1.f / l;
-            if (!whole) {
-              float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
-              prow[head] = m;
-              prow[64 + head] = l;
-            } else if (lse) {
-              lse[(long long)row * 64 + head] = log_sum(m, l);
-            }
+        if (!ok || (seg > 1 && !(ok = group_wait(bar(kBarOFree), uint32_t(seg) & 1u)))) break;
+        float l, l1;
+        f2_unpack(l2, l, l1);
+        l += l1;
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (part == 0) red[64 * w2 + head] = l;
+        named_bar_sync(1, 256);
+        if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
+          l = red[head] + red[64 + head];
+          linv_s[head] = l == 0.f ? 0.f : 1.f / l;
+          if (!whole) {
+            float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
+            prow[head] = m;
+            prow[64 + head] = l;
+          } else if (lse) {
+            lse[(long long)row * 64 + head] = log_sum(m, l);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarLFull));
-          if (more && !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg - 1) & 1u))) break;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarLFull));
+        if (more && !(ok = group_wait(bar(kBarQEmpty), uint32_t(seg - 1) & 1u))) break;
         if (!more) break;
         // --- the query's codes into tensor memory (lane = row of the A operand): 128 dims at a time, through shared memory
         // in two halves of 64, then the rope half into shared memory.  Eight lanes read 128 bytes of a head.
@@ -808,15 +861,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarQFull));
-
-        nt = walk.segment();
-        row = walk.t;
-        whole = nt == walk.ntiles;
-        head_part = walk.tile == 0;
-        walk.advance(nt);
       }
-      // --- the first row's scale, or the next one's while the first scores are made: 2^-e with max |q| <= 448 2^e, eight
-      // heads a warp.  An infinite or NaN value (codes have no infinity) makes all of the head's codes NaN.
+      nt = walk.segment();
+      row = walk.t;
+      whole = nt == walk.ntiles;
+      head_part = walk.tile == 0;
+      walk.advance(nt);
+      // --- the next row's scale, while this one's first scores are made: eight heads a warp
       if (walk.left > 0) {
         uint32_t amax[8];
         const uint16_t* qw = q + ((long long)walk.t * 64 + 8 * sw) * 576;
@@ -830,11 +881,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t a = __reduce_max_sync(0xffffffffu, max(amax[i] << 16, amax[i] & 0xffff0000u));
-          const int e = max(int(a >> 23) - 135 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-          if (lane == 0) qinv_s[8 * sw + i] = a < 0x7f800000u ? pow2f(-e) : __uint_as_float(0x7fc00000u);
+          if (lane == 0) qinv_s[8 * sw + i] = query_scale(a);
         }
       }
-      if (seg < 0) continue;
       // --- the row's tiles
       const f32x2 g2 = f2_pack(g, g);
       float off = 0.f, most = -INFINITY;  // kPgShift - m, and the x that asks for a new m
