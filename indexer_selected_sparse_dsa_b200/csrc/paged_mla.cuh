@@ -1022,13 +1022,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
                                                                         const float* __restrict__ part,
                                                                         __nv_bfloat16* __restrict__ o_lat,
                                                                         float* __restrict__ lse) {
-  __shared__ int list[kPgMaxGrid], warp_count[kMergeThreads / 32];
+  __shared__ int3 list[kPgMaxGrid];  // CTA, row, parts
+  __shared__ int warp_count[kMergeThreads / 32];
   pdl_wait();
   pdl_trigger();
   static_assert(kPgMaxGrid <= kMergeThreads, "a thread looks at one CTA");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool split = int(threadIdx.x) < ctas && meta[threadIdx.x].x >= 0;
-  const uint32_t votes = __ballot_sync(0xffffffffu, split);
+  const int2 mine = int(threadIdx.x) < ctas ? meta[threadIdx.x] : make_int2(-1, 0);
+  const uint32_t votes = __ballot_sync(0xffffffffu, mine.x >= 0);
   if (lane == 0) warp_count[warp] = __popc(votes);
   __syncthreads();
   int before = 0, rows = 0;
@@ -1037,30 +1038,43 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
     before += w < warp ? warp_count[w] : 0;
     rows += warp_count[w];
   }
-  if (split) list[before + __popc(votes & ((1u << lane) - 1u))] = threadIdx.x;
+  if (mine.x >= 0) list[before + __popc(votes & ((1u << lane) - 1u))] = make_int3(threadIdx.x, mine.x, mine.y);
   __syncthreads();
   for (int u = blockIdx.x * (kMergeThreads / 32) + warp; u < rows * 256; u += gridDim.x * (kMergeThreads / 32)) {
-    const int cta = list[u >> 8], h = (u >> 2) & 63, d = 128 * (u & 3) + 4 * lane;
-    const int2 sp = meta[cta];  // row, parts
-    auto at = [&](int i) { return part + (long long)(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * kPartFloats; };
-    float M = -INFINITY;
-    for (int i = lane; i < sp.y; i += 32) M = fmaxf(M, at(i)[64 * 512 + h]);
+    const int h = (u >> 2) & 63, d = 128 * (u & 3) + 4 * lane;
+    const int3 sp = list[u >> 8];
+    const int parts = sp.z;
+    auto at = [&](int i) { return part + (long long)(i == 0 ? 2 * sp.x + 1 : 2 * (sp.x + i)) * kPartFloats; };
+    // lane i holds the weight of part i0 + i (0 behind the last); the parts' own loads do not wait for it
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4*>(at(min(k, parts - 1)) + h * 512 + d);
+    float m = -INFINITY, l = 0.f;
+    if (lane < parts) {
+      m = at(lane)[64 * 512 + h];
+      l = at(lane)[64 * 512 + 64 + h];
+    }
+    float M = m;
+    for (int i = 32 + lane; i < parts; i += 32) M = fmaxf(M, at(i)[64 * 512 + h]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float M0 = M == -INFINITY ? 0.f : M;
     float den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < sp.y; i0 += 32) {
-      // lane i holds the weight of part i0 + i (0 behind the last), so the parts' own loads need not wait for it
-      const bool has = i0 + lane < sp.y;
-      const float w = has ? fast_exp2(at(i0 + lane)[64 * 512 + h] - M0) : 0.f;
-      const float wl = has ? w * at(i0 + lane)[64 * 512 + 64 + h] : 0.f;
-      den += wl;
-      const int n = min(32, sp.y - i0);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const bool has = i0 + lane < parts;
+      if (i0 > 0 && has) {
+        m = at(i0 + lane)[64 * 512 + h];
+        l = at(i0 + lane)[64 * 512 + 64 + h];
+      }
+      const float w = has ? fast_exp2(m - M0) : 0.f;
+      den += has ? w * l : 0.f;
+      const int n = min(32, parts - i0);
       for (int j = 0; j < n; j += 8) {
-        float4 x[8];
+        if (i0 + j > 0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4*>(at(i0 + min(j + k, n - 1)) + h * 512 + d);
+          for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4*>(at(i0 + min(j + k, n - 1)) + h * 512 + d);
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
@@ -1078,10 +1092,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
     const float inv = den == 0.f ? 0.f : 1.f / den;
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(o_lat + ((long long)sp.x * 64 + h) * 512 + d) =
+    *reinterpret_cast<uint2*>(o_lat + ((long long)sp.y * 64 + h) * 512 + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     if (lse && (u & 3) == 0 && lane == 0)
-      lse[(long long)sp.x * 64 + h] = log_sum(M0, den);
+      lse[(long long)sp.y * 64 + h] = log_sum(M0, den);
   }
 }
 
