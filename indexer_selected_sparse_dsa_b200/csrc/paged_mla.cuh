@@ -32,9 +32,9 @@
 // of operands out for S, 128 KB of widened values in and 192 KB out for O, 16 KB of
 // P: some 4300 cycles at 128 bytes each, against 3500 that a tile's 82 KB take from
 // HBM.  Measured 5400 cycles a tile, 11000 more where a CTA goes on to another query
-// row.  64 sequences of 2K to 16K positions, one token: 137 us (3.1 TB/s, 0.47 of
-// the measured copy rate); 512 tokens over 8192 positions: 0.79 ms (820 TFLOP/s,
-// 0.51 of the measured bf16 rate); 64 x 2048 selected rows: 53 us.
+// row.  64 sequences of 2K to 16K positions, one token: 130 us (3.2 TB/s, 0.50 of
+// the measured copy rate); 512 tokens over 8192 positions: 0.81 ms (800 TFLOP/s,
+// 0.50 of the measured bf16 rate); 64 x 2048 selected rows: 49 us.
 //
 // One CTA walks an equal share of all 128-key tiles of the batch (a change of the
 // query row counts as two more), query row after query row; a row that ends in another CTA leaves partial sums that
@@ -145,6 +145,7 @@ struct TileWalk {
     left = tiles;
     row_end = cu_q[b + 1];
     enter_row();
+    if (tile == ntiles) advance(0);
   }
   // the tiles of this CTA in the current row
   __device__ __forceinline__ int segment() const { return min(ntiles - tile, left); }
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   // 62 us, 52 and 51 us.
   {
     longlong2* sums = reinterpret_cast<longlong2*>(smem);  // the warps' sums, in the rope half's room
+    int* longest_s = reinterpret_cast<int*>(sums + 32);
     const int per = (c.batch + kPgThreads - 1) / kPgThreads;
     const int b0 = min(int(threadIdx.x) * per, c.batch), b1 = min(b0 + per, c.batch);
     auto tiles = [&](int b, int& q0, int& nq, long long& len, bool report) {
@@ -314,13 +316,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int q0, nq;
     long long len;
     longlong2 mine = make_longlong2(0, 0);  // tiles, rows
+    int longest = 0;                        // tiles of a row
     for (int b = b0; b < b1; ++b) {
       mine.x += tiles(b, q0, nq, len, blockIdx.x == 0);
       mine.y += nq;
+      if (nq > 0) longest = max(longest, topk_tiles ? topk_tiles : int((max(len, 1ll) + 127) >> 7));
     }
     const longlong2 incl = scan(mine);
-    if (lane == 31) sums[warp] = incl;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+      sums[warp] = incl;
+      longest_s[warp] = longest;
+    }
     __syncthreads();
+    longest = __reduce_max_sync(0xffffffffu, lane < kPgThreads / 32 ? longest_s[lane] : 0);
     const longlong2 all = scan(lane < kPgThreads / 32 ? sums[lane] : make_longlong2(0, 0));
     const long long all_tiles = __shfl_sync(0xffffffffu, all.x, 31);
     const long long all_rows = __shfl_sync(0xffffffffu, all.y, 31);
@@ -328,6 +337,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const longlong2 before = make_longlong2(__shfl_sync(0xffffffffu, all.x, wb), __shfl_sync(0xffffffffu, all.y, wb));
     const long long cost = all_tiles > gridDim.x ? kPgRowCost : 0;  // (at most one tile each: nothing to balance)
     const long long share = (all_tiles + cost * all_rows + gridDim.x - 1) / gridDim.x;
+    // Whole rows only, a CTA taking those that begin in its share, where that makes the longest walk little longer: by one
+    // tile, and by up to four more as more CTAs would leave partial results.  (64 rows of 256, 512, 1024 keys: 22.5, 28.2,
+    // 35.6 us split, 17.1, 23.0, 34.3 us whole; a chunk of 400 rows of 2048: 131 and 120 us; one row of 300 keys stays
+    // split, 14.3 us against 17.6.)
+    const long long ctas = gridDim.x;
+    const bool whole_rows =
+        (longest + cost) * ((all_rows + ctas - 1) / ctas) <= share + 1 + 5 * min(all_tiles, ctas) / kPgMaxGrid;
     if (threadIdx.x == 64) start_s[3] = int(min(share, 1ll << 30));  // (a row has less than 2^24 tiles)
     const long long x0 = incl.x - mine.x + (warp ? before.x : 0), y0 = incl.y - mine.y + (warp ? before.y : 0);
 #pragma unroll 1
@@ -345,7 +361,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             else hi = mid;
           }
           const long long first = tiles_of(nq, len, topk_tiles, lo);
-          const int tile = int(max(0ll, g - at - first - cost * (lo + 1)));
+          const long long off = g - at - first - cost * lo;
+          const int tile = int(!whole_rows ? max(0ll, off - cost)
+                               : off == 0  ? 0
+                                           : tiles_of(nq, len, topk_tiles, lo + 1) - first);  // (the next row's begin)
           if (e == 0) {
             start_s[0] = b;
             start_s[1] = q0 + lo;

@@ -350,6 +350,27 @@ def test_a_position_selected_twice_counts_twice():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new, lens", [
+    ([1] * 64, [100 + 9 * b for b in range(64)]),                  # whole rows: one of up to six tiles a CTA
+    ([1] * 150, [130 + 2 * b for b in range(150)]),                # more rows than CTAs
+    ([3] * 110, [5 + 3 * b for b in range(110)]),                  # several short rows a CTA
+    ([1] * 20 + [0, 0] + [1] * 20, [300] * 20 + [0, 77] + [500] * 20),
+    ([1, 1, 1] + [1] * 60, [6000, 129, 128] + [20] * 60),          # long and short ones: split
+    ([40, 0, 1, 90], [4000, 3, 2500, 700]),
+])
+def test_rows_shared_out_over_the_ctas(new, lens):
+    c = Batch(new, lens, 32, seed=25)
+    o, lse = run_dense(c)
+    B.dsa_sync_status()
+    check_attention(c, o, lse)
+    for topk in (100, 256, 900):
+        idx = selection(c, topk, seed=topk, holes=0.1)
+        o, lse = run_selected(c, idx)
+        B.dsa_sync_status()
+        check_attention(c, o, lse, idx)
+
+
+@pytest.mark.gpu
 def test_sequences_may_share_pages():
     """A common prefix of four pages, read by both sequences."""
     import torch
