@@ -606,6 +606,38 @@ def test_on_another_stream_the_calls_follow_each_other():
 
 
 @pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls on two streams, a workspace each, with nothing between them: what each gives alone, bit for bit."""
+    import torch
+    cs = [Batch([1] * 40, [1500 + 20 * b for b in range(40)], 16, seed=27), Batch([60, 3], [900, 4000], 64, seed=28)]
+    picks = [torch.from_numpy(selection(c, 700, seed=29)).cuda() for c in cs]
+    ws = [B.workspace(B.DSA_OP_PAGED_MLA, c.T, c.table.shape[1] * c.page, 0) for c in cs]
+
+    def calls(k, outs, stream):
+        c = cs[k]
+        B.dsa_paged_mla_attn(c.q, *c.plan, c.kv8, c.kv_scale, SCALE, *outs[0], ws[k], stream=stream)
+        B.dsa_paged_sparse_mla_attn(c.q, *c.plan, picks[k], c.kv8, c.kv_scale, SCALE, *outs[1], ws[k], stream=stream)
+
+    alone = [[c.outputs(), c.outputs()] for c in cs]
+    for k in range(2):
+        calls(k, alone[k], None)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    both = [[[c.outputs(), c.outputs()] for c in cs] for _ in range(4)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for outs in both:
+        for k in (0, 1):
+            calls(k, outs[k], streams[k])
+    for st in streams:
+        B.dsa_sync_status(st)
+    for outs in both:
+        for k in range(2):
+            for got, want in zip(outs[k], alone[k]):
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
 def test_cache_larger_than_32_bit_offsets():
     """A sequence in the last pages of a cache of more than 2^32 bytes."""
     import torch
