@@ -290,10 +290,14 @@ def _raw_stream(stream, dev):
 
 def _paged_sizes(seq_len, page_table, kv8):
     """(batch, max_pages, n_pages, page_size); a wrong number of dimensions is found here, wrong sizes by _check_all."""
-    for t, nd, name in ((seq_len, 1, "seq_len"), (page_table, 2, "page_table"), (kv8, 3, "kv8")):
-        if getattr(t, "ndim", None) != nd:
-            raise TypeError(f"{name} must be a tensor of {nd} dimension{'s' if nd > 1 else ''}")
-    return seq_len.shape[0], page_table.shape[1], kv8.shape[0], kv8.shape[1]
+    try:
+        (batch,), (_, max_pages), (n_pages, page_size, _) = seq_len.shape, page_table.shape, kv8.shape
+    except (AttributeError, TypeError, ValueError):
+        for t, nd, name in ((seq_len, 1, "seq_len"), (page_table, 2, "page_table"), (kv8, 3, "kv8")):
+            if getattr(t, "ndim", None) != nd:
+                raise TypeError(f"{name} must be a tensor of {nd} dimension{'s' if nd > 1 else ''}") from None
+        raise
+    return batch, max_pages, n_pages, page_size
 
 
 def dsa_cache_write(rows, cu_q, seq_len, page_table, kv8, kv_scale, stream=None):
