@@ -14,10 +14,13 @@
 //
 // Values as fp16.  A code is exact in fp16, and a probability rounded to fp16
 // (2^-11) is eight times closer than one in bf16.  The row's 2^k goes into the
-// probability: with y = S log2(e) + k_s, u_s = 2^(y - m + 4) where m follows
-// the maximum of y in whole numbers, at most 11 behind: u is at most 2^15, and
-// what fp16 cannot hold is 2^-29 of the largest; sum u code is the numerator,
-// sum u 2^-k_s (fp32, u before rounding) the denominator.
+// probability: with y = S log2(e) + k_s, u_s = 2^(y - m + 28) where m follows
+// the maximum of y in whole numbers, at most 11 behind.  sum 2^-24 u code is the
+// numerator: 2^-24 u is at most 2^15, and what fp16 cannot hold of it is 2^-29 of
+// the largest.  sum u 2^-k_s (fp32, u before rounding) is the denominator, where a
+// row of the smallest scale may weigh as much as one of the largest with a u
+// 2^-120 of its: fp32 holds u down to 2^-126, 2^-154 of the largest, so what is
+// lost of the denominator is below 2^-34 of it a key.
 //
 // Shared memory carries no query: hi and lo lie in tensor memory as the A operand
 // (lanes 0..15 of each quarter the hi codes of 16 heads, lanes 16..31 their lo
@@ -71,8 +74,9 @@ constexpr int kPgVSlots = 3;          // of 128 dims: one product runs, one is r
 constexpr int kPgRows = 4;            // tiles whose keys are described
 constexpr int kPgRowCost = 2;         // what a CTA's change to another query row costs, in tiles
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
-constexpr float kPgShift = 4.f;       // log2 of the probability at the running maximum ...
-constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much (fp16 ends at 2^16)
+constexpr float kPgShift = 28.f;      // log2 of u at the running maximum ...
+constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much ...
+constexpr float kPgHalf = 1.f / (1 << 24);  // ... and u's factor in the value product (fp16 ends at 2^16)
 
 constexpr int kPgQR = 0;                                     // the query's rope half: 128 rows (hi rows; lo rows are 0) x 64 bf16
 constexpr int kPgP = kPgQR + kPgSlot;                        // 2 chunks of 64 heads x 64 keys fp16
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         named_bar_sync(1, 256);
         if (sw < 4 && part == 0) {  // (l is 0 or NaN where there is no m)
           l = red[head] + red[64 + head];
-          linv_s[head] = l == 0.f ? 0.f : 1.f / l;
+          linv_s[head] = l == 0.f ? 0.f : 1.f / (l * kPgHalf);
           if (!whole) {
             float* prow = part_out + (long long)(2 * blockIdx.x + (head_part ? 1 : 0)) * kPartFloats + 64 * 512;
             prow[head] = m;
@@ -955,9 +959,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           if (part == 0) red[64 * w2 + head] = top;
           named_bar_sync(1, 256);
           const float mt = floorf(fmaxf(red[head], red[64 + head]) - off);
-          float al = 1.f;
+          // The sum takes 2^(m - mt) in two factors: rows of unlike scales may leave more than fp32's exponents between
+          // the maxima, and less between the sums.
+          float al = 1.f, al2 = 1.f;
           if (mt > m && (m == -INFINITY || mt >= m + kPgLazy)) {
-            al = m == -INFINITY ? 0.f : fast_exp2(m - mt);
+            const float e = floorf(0.5f * (m - mt));
+            al = m == -INFINITY ? 0.f : fast_exp2(e);
+            al2 = m == -INFINITY ? 0.f : fast_exp2(m - mt - e);
             const float d = kPgShift - mt - off;
             const f32x2 d2 = f2_pack(d, d);
 #pragma unroll
@@ -966,11 +974,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             off = kPgShift - mt;
             most = kPgShift + kPgLazy;
           }
-          l2 = f2_mul(l2, f2_pack(al, al));
+          l2 = f2_mul(f2_mul(l2, f2_pack(al, al)), f2_pack(al2, al2));
+          al *= al2;
           if (sw < 4 && part == 0) alpha_s[head] = al;
           resc = bar_red_or(1, 256, t > 0 && al != 1.f);  // also publishes alpha_s
         }
-        // u = 2^x, rounded to fp16 for the value product; the sum takes it unrounded
+        // u = 2^x; 2^-24 u rounded to fp16 for the value product; the sum takes it unrounded
         uint32_t w[16];
 #pragma unroll
         for (int i0 = 0; i0 < 16; i0 += 2) {
@@ -981,7 +990,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             f2_unpack(x[i0 + e], a0, a1);
             a0 = fast_exp2(a0);
             a1 = fast_exp2(a1);
-            l2 = f2_fma(f2_pack(a0, a1), e ? inv.y : inv.x, l2);
+            const f32x2 u = f2_pack(a0, a1);
+            l2 = f2_fma(u, e ? inv.y : inv.x, l2);
+            f2_unpack(f2_mul(u, f2_pack(kPgHalf, kPgHalf)), a0, a1);
             const __half2 p = __floats2half2_rn(a0, a1);
             w[i0 + e] = *reinterpret_cast<const uint32_t*>(&p);
           }
@@ -1033,7 +1044,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   }
 }
 
-// Rows split over CTAs: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  The row that CTA c of the
+// Rows split over CTAs: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M - 24) l_i.  The row that CTA c of the
 // attention ended inside: its own partial result 1, then partial result 0 of the CTAs behind it.  Every block lists the
 // split rows; a warp takes 128 dims of one head of one of them at a time, with eight partial results in flight.
 constexpr int kMergeThreads = 256;
@@ -1087,7 +1098,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
         l = at(i0 + lane)[64 * 512 + 64 + h];
       }
       const float w = has ? fast_exp2(m - M0) : 0.f;
-      den += has ? w * l : 0.f;
+      const float e = floorf(0.5f * (m - M0));  // (in two factors: 2^(m - M0) may pass fp32's exponents where l makes up for it)
+      den += !has ? 0.f : m == -INFINITY ? w * l : l * fast_exp2(e) * fast_exp2(m - M0 - e);
       const int n = min(32, parts - i0);
       for (int j = 0; j < n; j += 8) {
         if (i0 + j > 0) {
@@ -1108,7 +1120,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = den == 0.f ? 0.f : 1.f / (den * kPgHalf);
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(o_lat + ((long long)sp.y * 64 + h) * 512 + d) =

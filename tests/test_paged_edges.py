@@ -1,0 +1,48 @@
+"""Paged latent cache and attention: values, plans and calls at the edges of what their description allows."""
+import numpy as np
+import pytest
+
+from indexer_selected_sparse_dsa_b200 import binding as B
+from paged_util import LATENT, ROW, ROW8, SCALE, Batch, quantise64
+from test_paged_cache import run_dense
+
+
+def put(c, b, pos, rows):
+    """Store latent rows (64-bit, bf16 values) at positions `pos` of sequence b, as dsa_cache_write does."""
+    import torch
+    codes, rope, scale = quantise64(rows)
+    at = torch.from_numpy(c.slots(b, pos)).cuda()
+    c.kv8.view(-1, ROW8)[at] = torch.cat([codes, rope.to(torch.bfloat16).view(torch.uint8)], 1)
+    c.kv_scale.view(-1)[at] = scale.float()
+
+
+# ------------------------------------------------------------------ scales far apart
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gap", [2.0, 8.0, 16.0])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("n", [100, 1000, 6000])
+def test_rows_of_the_largest_and_the_smallest_scale(n, first, gap):
+    """One position of scale 2^60 and many zero rows (2^-60), whose scores are `gap` below its own: together they weigh as
+    much as the softmax says.  What is looked at: o = p v and lse.  The scores come from the rope half alone (the latent
+    half of the query is 0, its products are exact), so besides the sums, 2^-17 of them, what is rounded is the
+    probability, 2^-11, and the result, 2^-8."""
+    import torch
+    c = Batch([1], [n], 16, seed=41)
+    one = 0 if first else n - 1
+    rows = torch.zeros(n, ROW, dtype=torch.float64, device="cuda")
+    rows[one, :LATENT] = 448.0 * 2.0 ** 60
+    rows[one, 100:LATENT] = 32.0 * 2.0 ** 60
+    rows[one, LATENT] = 1.0
+    put(c, 0, np.arange(n), rows)
+    assert set(c.kv_scale.view(-1)[torch.from_numpy(c.slots(0, np.arange(n))).cuda()].tolist()) == {2.0 ** 60, 2.0 ** -60}
+    c.q[:, :, :] = 0
+    c.q[:, :, LATENT] = gap / SCALE
+    o, lse = run_dense(c)
+    B.dsa_sync_status()
+    x = torch.zeros(n, dtype=torch.float64)
+    x[one] = gap
+    want = torch.softmax(x, 0)[one].item() * rows[one, :LATENT]
+    e = 2.0 ** -16 * gap + 2.0 ** -20
+    assert bool(((o[0].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16 + 2 * e) * want.abs()).all())
+    assert float((lse[0].double() - torch.logsumexp(x, 0).item()).abs().max()) <= e + 2.0 ** -16
