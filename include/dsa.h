@@ -291,6 +291,9 @@ DSA_API int dsa_indexer_scores_noalloc(const dsa_bf16* q_I, const dsa_bf16* w, c
  *     kv_scale[row]     = 2^k
  * Only the e4m3 code is a rounding: the rope half is exact for magnitudes in
  * [2^-66, 2^67], and a code times 2^k is exact in bf16.
+ * An infinite k_rope stays infinite: to the attention, a head whose product with
+ * it is -inf gives that position the weight 0; the heads of the others (+inf, or
+ * 0 * inf) have no finite result.
  *
  * Batch.  `batch` sequences; sequence b's cache is pages page_table[b, 0 ..],
  * position s in row page_table[b, s / page_size] * page_size + s % page_size.

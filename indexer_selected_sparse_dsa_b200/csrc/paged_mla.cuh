@@ -9,8 +9,11 @@
 // q = 2^e (hi + lo / 16), both e4m3 (4 + 4 significant bits: exact for values
 // within 2^5 of the head's largest, never off by more than 2^-22 of it), so
 // the 8-bit tensor path multiplies the cache's codes as they lie in memory:
-// M = 128 rows, 64 of hi and 64 of lo.  The rope half follows in bf16 on top of
-// the hi rows.  2^k_s, 2^e and the scale are applied to the fp32 sums.
+// M = 128 rows, 64 of hi and 64 of lo.  The rope half follows in bf16 on top: half
+// of the query on the hi rows and eight times it on the lo rows, both exact.  (Zero
+// lo rows would make NaN of an infinite rope value, where a head's -inf is weight 0;
+// hi rows alone, M = 64, took 1.5% more time for a chunk.)  2^k_s, 2^e and the scale
+// are applied to the fp32 sums.
 //
 // Values as fp16.  A code is exact in fp16, and a probability rounded to fp16
 // (2^-11) is eight times closer than one in bf16.  The row's 2^k goes into the
@@ -78,7 +81,7 @@ constexpr float kPgShift = 28.f;      // log2 of u at the running maximum ...
 constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much ...
 constexpr float kPgHalf = 1.f / (1 << 24);  // ... and u's factor in the value product (fp16 ends at 2^16)
 
-constexpr int kPgQR = 0;                                     // the query's rope half: 128 rows (hi rows; lo rows are 0) x 64 bf16
+constexpr int kPgQR = 0;                                     // the query's rope half: 128 rows (1/2 and 8 times it) x 64 bf16
 constexpr int kPgP = kPgQR + kPgSlot;                        // 2 chunks of 64 heads x 64 keys fp16
 constexpr int kPgK = kPgP + kPgSlot;
 constexpr int kPgV = kPgK + kPgKSlots * kPgSlot;             // a slot: two chunks of 128 keys x 64 dims fp16
@@ -218,6 +221,9 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, f32x2 inv) {
   f2_unpack(f2_mul(f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), inv), a, b);
   const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&o);
+}
+__device__ __forceinline__ uint4 scale_bf16x8(const uint4& x, f32x2 inv) {
+  return make_uint4(scale_bf16x2(x.x, inv), scale_bf16x2(x.y, inv), scale_bf16x2(x.z, inv), scale_bf16x2(x.w, inv));
 }
 
 // Four query values (two words of bf16 pairs) times inv as hi codes and lo codes: v = hi + lo / 16.  v goes through
@@ -443,9 +449,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       *reinterpret_cast<uint2*>(to + 16 * 512) = lo;
     }
     uint8_t* rope = smem + kPgQR + row * 128 + ((l8 ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(rope) = make_uint4(scale_bf16x2(x[8].x, inv), scale_bf16x2(x[8].y, inv),
-                                                 scale_bf16x2(x[8].z, inv), scale_bf16x2(x[8].w, inv));
-    *reinterpret_cast<uint4*>(rope + 16 * 128) = make_uint4(0, 0, 0, 0);  // the lo rows of the rope half stay zero
+    *reinterpret_cast<uint4*>(rope) = scale_bf16x8(x[8], f2_pack(0.5f * inv1, 0.5f * inv1));
+    *reinterpret_cast<uint4*>(rope + 16 * 128) = scale_bf16x8(x[8], f2_pack(8.f * inv1, 8.f * inv1));
     named_bar_sync(2, 512);
     const int own = 32 * (warp & 3) + lane, piece = (warp >> 2) - 1;
 #pragma unroll
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       }
       int* row_s = reinterpret_cast<int*>(keys_of(n)) + lane;
       float* cs_s = reinterpret_cast<float*>(row_s) + 128;
-      // A place without a key takes the row of one that has: it is read with weight 0, and what other rows of the cache
+      // A place without a key takes the row of one that has: its score gets -inf added, and what other rows of the cache
       // hold (NaN perhaps) is not read.  -1 throughout where the tile has no key.
       const int some = __reduce_max_sync(0xffffffffu, max(max(row0[0], row0[1]), max(row0[2], row0[3])));
 #pragma unroll
@@ -572,7 +577,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int e = int(__float_as_uint(sc0[i]) >> 23);  // k + 127
         const bool has = row0[i] >= 0;
         row_s[32 * i] = has ? row0[i] : some;
-        cs_s[32 * i] = sc0[i] * scale_log2;
+        cs_s[32 * i] = has ? sc0[i] * scale_log2 : 0x1p-24f;  // (any factor but 0, which times an infinite score is NaN)
         cs_s[128 + 32 * i] = has ? float(e - 127) : -INFINITY;
         cs_s[256 + 32 * i] = has ? pow2f(127 - e) : 0.f;
       }
@@ -874,9 +879,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int h = hd + 4 * k, row = 32 * (h >> 4) + (h & 15);
-            *reinterpret_cast<uint4*>(smem + kPgQR + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
-                make_uint4(scale_bf16x2(x[2 + k].x, inv[k]), scale_bf16x2(x[2 + k].y, inv[k]),
-                           scale_bf16x2(x[2 + k].z, inv[k]), scale_bf16x2(x[2 + k].w, inv[k]));
+            uint8_t* to = smem + kPgQR + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = scale_bf16x8(x[2 + k], f2_mul(inv[k], f2_pack(0.5f, 0.5f)));
+            *reinterpret_cast<uint4*>(to + 16 * 128) = scale_bf16x8(x[2 + k], f2_mul(inv[k], f2_pack(8.f, 8.f)));
           }
         }
         tmem_wait_st();

@@ -1,10 +1,12 @@
 """Paged latent cache and attention: values, plans and calls at the edges of what their description allows."""
+import math
+
 import numpy as np
 import pytest
 
 from indexer_selected_sparse_dsa_b200 import binding as B
-from paged_util import LATENT, ROW, ROW8, SCALE, Batch, quantise64
-from test_paged_cache import run_dense
+from paged_util import HEADS, LATENT, ROW, ROW8, SCALE, Batch, quantise64
+from test_paged_cache import run_dense, run_selected
 
 
 def put(c, b, pos, rows):
@@ -46,3 +48,34 @@ def test_rows_of_the_largest_and_the_smallest_scale(n, first, gap):
     e = 2.0 ** -16 * gap + 2.0 ** -20
     assert bool(((o[0].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16 + 2 * e) * want.abs()).all())
     assert float((lse[0].double() - torch.logsumexp(x, 0).item()).abs().max()) <= e + 2.0 ** -16
+
+
+# ------------------------------------------------------------------ infinite rope values
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[300], [3000], [129, 700], [90]])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_an_infinite_rope_value_weighs_nothing_where_its_score_is_minus_infinity(lens, bad):
+    """Heads whose product with it is -inf give its position the weight 0, as the softmax does; the others, +inf, have no
+    finite result.  The row is the highest of the cache in its tile, the one that places without a key read too."""
+    import torch
+    c = Batch([1] * len(lens), lens, 16, seed=40)
+    c.q[:, :, LATENT:] = torch.where(c.q[:, :, LATENT:] == 0, 1, c.q[:, :, LATENT:])
+    idx = np.full((c.T, max(lens)), -1, np.int32)
+    for b, m in enumerate(lens):
+        tile = np.arange((m - 1) // 128 * 128, m)
+        hit = int(tile[np.argmax(c.slots(b, tile))])
+        c.kv8.view(-1, ROW8)[int(c.slots(b, hit)), LATENT:].view(torch.bfloat16)[9 + b] = bad
+        idx[b, :m - 1] = np.delete(np.arange(m), hit)
+    ro, rl, to, tl = c.reference(idx)                                 # without that position
+    wide = np.full((c.T, max(lens) + 40), -1, np.int32)               # with it, and with empty slots
+    for b, m in enumerate(lens):
+        wide[b, 20:20 + m] = np.arange(m)
+    for o, lse in (run_dense(c), run_selected(c, wide) if wide.shape[1] <= 2048 else run_dense(c)):
+        B.dsa_sync_status()
+        for t in range(c.T):
+            gone = (torch.sign(c.q[t, :, LATENT + 9 + t].float()) * bad) < 0
+            assert 0 < int(gone.sum()) < HEADS
+            assert bool(((o[t].double() - ro[t]).abs() <= to[t])[gone].all())
+            assert bool(((lse[t].double() - rl[t]).abs() <= tl[t])[gone].all())
+            assert not bool(o[t, ~gone].isfinite().any()) and not bool(lse[t, ~gone].isfinite().any())
