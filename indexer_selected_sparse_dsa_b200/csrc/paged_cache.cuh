@@ -61,12 +61,12 @@ __device__ __forceinline__ int owner_of(const int32_t* __restrict__ cu_q, int ba
 }
 
 // Positions that query row t of sequence b sees: 0 .. seen - 1, its own the last.
-// 0 (and the status bit) where cu_q, seq_len and the page table do not describe it.
+// 0 (and the status bit) where cu_q, T, seq_len and the page table do not describe it.
 __device__ __forceinline__ int seen_by(const PagedCache& c, const int32_t* __restrict__ cu_q,
-                                       const int32_t* __restrict__ seq_len, int b, int t) {
+                                       const int32_t* __restrict__ seq_len, int T, int b, int t) {
   const int q0 = cu_q[b], q1 = cu_q[b + 1], len = seq_len[b];
   const long long seen = (long long)len - ((long long)q1 - t) + 1;
-  if (q0 < 0 || t < q0 || t >= q1 || seen < 1 || len > max_positions(c)) {
+  if (q0 < 0 || t < q0 || t >= q1 || q1 > T || seen < 1 || len > max_positions(c)) {
     raise_status(kStatusBadRow);
     return 0;
   }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kCacheThreads)
 
   const int b = owner_of(cu_q, c.batch, t);
   if (b >= c.batch || (b == 0 && t < cu_q[0])) return;  // behind the last sequence, or before the first
-  const int seen = seen_by(c, cu_q, seq_len, b, t);
+  const int seen = seen_by(c, cu_q, seq_len, T, b, t);
   const int row = seen > 0 ? cache_row(c, b, seen - 1) : -1;
   if (row < 0) return;
 

@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 
 from indexer_selected_sparse_dsa_b200 import binding as B
-from paged_util import HEADS, LATENT, ROW, ROW8, SCALE, Batch, quantise64
-from test_paged_cache import run_dense, run_selected
+from paged_util import HEADS, LATENT, ROW, ROW8, SCALE, Batch, check_attention, quantise64
+from test_paged_cache import bad_status, run_dense, run_selected
 
 
 def put(c, b, pos, rows):
@@ -79,3 +79,50 @@ def test_an_infinite_rope_value_weighs_nothing_where_its_score_is_minus_infinity
             assert bool(((o[t].double() - ro[t]).abs() <= to[t])[gone].all())
             assert bool(((lse[t].double() - rl[t]).abs() <= tl[t])[gone].all())
             assert not bool(o[t, ~gone].isfinite().any()) and not bool(lse[t, ~gone].isfinite().any())
+
+
+# ------------------------------------------------------------------ plans that do not fit
+
+@pytest.mark.gpu
+def test_a_sequence_whose_rows_pass_the_end():
+    """Only cu_q[batch] is above T: that sequence is skipped by the writer as by the attention, with the status bit."""
+    import torch
+    c = Batch([2, 3], [50, 60], 16, seed=42)
+    out = run_dense(c)
+    new = torch.randn(5, ROW, device="cuda").bfloat16()
+    c.cu_q = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    got = c.outputs()
+    bad_status(lambda: run_dense(c, got))
+    assert torch.equal(got[0][:2], out[0][:2]) and torch.equal(got[1][:2], out[1][:2])
+    before = c.kv8.clone()
+    bad_status(lambda: B.dsa_cache_write(new, *c.plan, c.kv8, c.kv_scale))
+    changed = (c.kv8 != before).any(2).view(-1).nonzero().flatten().cpu().tolist()
+    assert set(changed) == {int(s) for s in c.slots(0, [48, 49])}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu,rows", [([0, 3, 1, 4], {0: (0, 47, 3), 3: (2, 69, 3)}),
+                                     ([0, 2, 1 << 30, 4], {0: (0, 48, 2), 1: (0, 49, 2)}),
+                                     ([-2, 1, 2, 4], {1: (1, 59, 1), 2: (2, 68, 2), 3: (2, 69, 2)})])
+def test_sequences_in_order_beside_others_that_are_not(cu, rows):
+    """Rows that one sequence in order has to itself come out and are written; nothing lies around the tensors' ends."""
+    import torch
+    c = Batch([2, 1, 1], [50, 60, 70], 16, seed=43)
+    c.cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o = torch.full((c.T + 4, HEADS, LATENT), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.T + 4, HEADS), 7.0, device="cuda")
+    bad_status(lambda: run_dense(c, (o[2:-2], lse[2:-2])))
+    for x in (o, lse):
+        assert bool((x[:2] == 7.0).all()) and bool((x[-2:] == 7.0).all())
+    alone = Batch([1], [1], 16, seed=43)
+    for t, (b, pos, _) in rows.items():
+        alone.q, alone.T, alone.new, alone.lens = c.q[t:t + 1], 1, [1], [pos + 1]
+        alone.kv8, alone.kv_scale, alone.table = c.kv8, c.kv_scale, c.table[b:b + 1]
+        check_attention(alone, o[2 + t:3 + t], lse[2 + t:3 + t])
+    new = torch.randn(c.T, ROW, device="cuda").bfloat16()
+    codes, rope, scale = quantise64(new.double())
+    want = torch.cat([codes, rope.to(torch.bfloat16).view(torch.uint8)], 1)
+    bad_status(lambda: B.dsa_cache_write(new, *c.plan, c.kv8, c.kv_scale))
+    for t, (b, pos, _) in rows.items():
+        at = int(c.slots(b, [pos])[0])
+        assert torch.equal(c.kv8.view(-1, ROW8)[at], want[t]) and float(c.kv_scale.view(-1)[at]) == float(scale[t])
