@@ -404,8 +404,9 @@ DSA_API int dsa_sync_status(dsa_stream_t stream);
  * operation it started finish, releases its resources and exits, and the
  * timeout bit reported by dsa_sync_status as DSA_ERR_TIMEOUT is raised; the
  * outputs of that call are then undefined, the CUDA context stays usable.
- * 0 restores the default (environment variable DSA_WAIT_LIMIT_NS, else
- * 1.5 s).  Takes effect for launches after the call; process-wide.
+ * (A waiting warp reads the clock every few microseconds.)  0 restores the
+ * default (environment variable DSA_WAIT_LIMIT_NS, else 1.5 s).  Takes effect
+ * for launches after the call; process-wide.
  */
 DSA_API void dsa_set_wait_limit_ns(unsigned long long ns);
 

@@ -77,6 +77,7 @@ constexpr int kPgVSlots = 3;          // of 128 dims: one product runs, one is r
 constexpr int kPgRows = 4;            // tiles whose keys are described
 constexpr int kPgRowCost = 2;         // what a CTA's change to another query row costs, in tiles
 constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
+constexpr unsigned long long kPgBriefNs = 8000;  // wait limits below it are brief: two failing tries
 constexpr float kPgShift = 28.f;      // log2 of u at the running maximum ...
 constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much ...
 constexpr float kPgHalf = 1.f / (1 << 24);  // ... and u's factor in the value product (fp16 ends at 2^16)
@@ -245,7 +246,7 @@ __device__ __forceinline__ void split_codes(uint32_t w0, uint32_t w1, f32x2 inv,
   lo = __byte_perm(d[0], d[1], 0x5410);
 }
 
-template <bool kSparse>
+template <bool kSparse, bool kBrief>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_mla_kernel(const uint16_t* __restrict__ q, int T, const int32_t* __restrict__ cu_q,
                      const int32_t* __restrict__ seq_len, const int32_t* __restrict__ idx, int topk,
@@ -400,18 +401,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   if (busy) walk.start(start_s, own_tiles);
   else if (threadIdx.x == 0) meta[blockIdx.x] = make_int2(-1, 0);
 
-  // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back after 4 us (measured), so
-  // the limit is counted in tries, and one shorter than a try gives up at once: five warps of four roles share a
-  // scheduler's instruction cache, and the code of 18 waits has to stay short (with the clock read in each, and loops
-  // unrolled, a tile took 7100 cycles).  Who gives up leaves its loop; the roles that wait for it run into their own limits.
-  const uint32_t tries = uint32_t(min(lim.ns / 4000, 1000000000ull)) + 1;
+  // A bounded wait of a whole warp; the lanes agree on its outcome.  A try that fails comes back after 4 us (measured, with
+  // any time hint), so a limit below two of them takes the kernel that looks without suspending.  (The clock costs up to
+  // 0.3% against counting the tries, which would need to know how long one takes.)  Who gives up leaves its loop; the roles
+  // that wait for it run into their own limits.
   auto warp_wait = [&](uint32_t b, uint32_t parity) {
-    uint32_t left = tries;
+    const unsigned long long t0 = globaltimer();
     bool done;
 #pragma unroll 1
-    do done = __all_sync(0xffffffffu, mbar_try_wait(b, parity)) != 0;
-    while (!done && --left);
-    return done && tries > 1;
+    do done = __all_sync(0xffffffffu, kBrief ? mbar_test_wait(b, parity) : mbar_try_wait(b, parity)) != 0;
+    while (!done && !__any_sync(0xffffffffu, globaltimer() - t0 >= lim.ns));
+    return done;
   };
   // The same for the softmax: one warp tries, and a barrier hands all 256 threads the outcome, so that they leave
   // together if they have to.
@@ -1150,9 +1150,12 @@ inline size_t paged_mla_ws_bytes(int T, int64_t max_keys) {
 
 cudaError_t prepare_paged_mla() {
   static_assert(kPgSmemAlloc <= 232448, "paged MLA shared memory exceeds the per-CTA limit");
-  cudaError_t e = cudaFuncSetAttribute(paged_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmemAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_mla_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmemAlloc);
+  for (auto* kernel : {paged_mla_kernel<false, false>, paged_mla_kernel<false, true>, paged_mla_kernel<true, false>,
+                       paged_mla_kernel<true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmemAlloc);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_paged_mla(const PagedMlaLaunch& p) {
@@ -1161,9 +1164,12 @@ cudaError_t launch_paged_mla(const PagedMlaLaunch& p) {
   int2* meta = static_cast<int2*>(p.ws);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kPgMetaBytes);
   auto* o = reinterpret_cast<__nv_bfloat16*>(p.o_lat);
-  cudaError_t e = launch_pdl(p.idx ? paged_mla_kernel<true> : paged_mla_kernel<false>, dim3(grid), dim3(kPgThreads),
-                             kPgSmemAlloc, p.stream, 1, p.q, p.T, p.cu_q, p.seq_len, p.idx, p.topk, p.cache,
-                             p.scale * 1.4426950408889634f, o, p.lse, meta, part, WaitLimit{p.wait_ns});
+  const bool brief = p.wait_ns < kPgBriefNs;
+  auto* kernel = p.idx ? (brief ? paged_mla_kernel<true, true> : paged_mla_kernel<true, false>)
+                       : (brief ? paged_mla_kernel<false, true> : paged_mla_kernel<false, false>);
+  cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kPgThreads), kPgSmemAlloc, p.stream, 1, p.q, p.T, p.cu_q, p.seq_len,
+                             p.idx, p.topk, p.cache, p.scale * 1.4426950408889634f, o, p.lse, meta, part,
+                             WaitLimit{p.wait_ns});
   if (e != cudaSuccess || grid == 1) return e;
   // at most one split row per CTA, 32 blocks' worth of warps each
   const unsigned blocks = grid * 32u < 4u * unsigned(p.sm_count) ? grid * 32u : 4u * unsigned(p.sm_count);

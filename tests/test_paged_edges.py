@@ -126,3 +126,54 @@ def test_sequences_in_order_beside_others_that_are_not(cu, rows):
     for t, (b, pos, _) in rows.items():
         at = int(c.slots(b, [pos])[0])
         assert torch.equal(c.kv8.view(-1, ROW8)[at], want[t]) and float(c.kv_scale.view(-1)[at]) == float(scale[t])
+
+
+# ------------------------------------------------------------------ short wait limits
+
+SHORT = r"""
+import sys
+sys.path[:0] = [ROOT, ROOT + "/tests"]
+from indexer_selected_sparse_dsa_b200 import binding as B
+from paged_util import Batch, check_attention, selection
+from test_paged_cache import run_dense, run_selected
+def limited(ns, call, c, *pick):
+    B.dsa_set_wait_limit_ns(ns)
+    out = c.outputs()
+    try:
+        call(c, *pick, out=out)
+        B.dsa_sync_status()
+        check_attention(c, *out, *pick)
+        return "OK"
+    except B.DSAError as e:
+        assert e.code == B.DSA_ERR_TIMEOUT, e
+        return "TIMEOUT"
+    finally:
+        B.dsa_set_wait_limit_ns(0)
+        check_attention(c, *call(c, *pick), *pick)
+        B.dsa_sync_status()
+seen = {}
+for new, lens in (([1, 6, 2], [3000, 700, 90]), ([60, 3], [2000, 9000])):
+    c = Batch(new, lens, 16, seed=30)
+    idx = selection(c, 300, seed=31)
+    for ns in LIMITS:
+        for call, pick in ((run_dense, ()), (run_selected, (idx,))):
+            seen.setdefault(ns, []).append(limited(ns, call, c, *pick))
+c = Batch([1], [1], 16, seed=32)
+in_time = [limited(3900, run_dense, c) for _ in range(20)]
+print("RESULT", all(s == "TIMEOUT" for s in seen[1]), all(s == "OK" for s in seen[200000]), "OK" in in_time, flush=True)
+"""
+
+
+@pytest.mark.gpu
+def test_a_short_limit_times_out_or_gives_the_result():
+    """Limits from a nanosecond to 0.2 ms over a few tiles a CTA: waits give up at the start, in the middle of the pipeline or
+    not at all.  A call that reports no timeout is right, and so is the next call after one that does.  No wait is complete
+    within 1 ns everywhere, none of so small a batch is 0.2 ms late, and one key's waits (2.5 us) are not 3.9 us late."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    limits = [1, 300, 1000, 2000, 3000, 4000, 5000, 6000, 7000, 8000, 9000, 10000, 12000, 14000, 16000, 20000, 200000]
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\nLIMITS = {limits!r}\n" + SHORT], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "RESULT True True True" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
