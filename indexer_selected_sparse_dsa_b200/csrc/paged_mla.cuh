@@ -61,6 +61,7 @@
 
 #include "internal.h"
 #include "paged_cache.cuh"
+#include "paged_share.cuh"
 #include "ptx.cuh"
 #include "sparse_mla.cuh"
 
@@ -75,8 +76,6 @@ constexpr int kPgKSlots = 5;          // the five chunks of a tile, each in a pl
 constexpr int kPgKGroups = 3;         // waited for together: codes 0..255, codes 256..511, rope
 constexpr int kPgVSlots = 3;          // of 128 dims: one product runs, one is ready, one is being widened
 constexpr int kPgRows = 4;            // tiles whose keys are described
-constexpr int kPgRowCost = 2;         // what a CTA's change to another query row costs, in tiles
-constexpr int kPgMaxGrid = 160;       // CTAs at most (the workspace is sized for it)
 constexpr unsigned long long kPgBriefNs = 8000;  // wait limits below it are brief: two failing tries
 constexpr float kPgShift = 28.f;      // log2 of u at the running maximum ...
 constexpr float kPgLazy = 11.f;       // ... which a score may pass by this much ...
@@ -123,12 +122,6 @@ __device__ __forceinline__ int seq_rows(const int32_t* __restrict__ cu_q, int T,
   return q1 - q0;
 }
 
-// sum of ceil(i / 128) over i = 1 .. n
-__device__ __forceinline__ long long tiles_below(long long n) {
-  const long long q = n >> 7, r = n & 127;
-  return 64 * q * (q + 1) + r * (q + 1);
-}
-
 // The batch's tiles as every role of a CTA walks them, in order: row t of
 // sequence b, tile `tile` of the row's `ntiles`, `left` tiles until the CTA's end.
 struct TileWalk {
@@ -173,15 +166,6 @@ struct TileWalk {
     }
   }
 };
-
-// Tiles of the first j query rows of a sequence with nq rows and length len (len < 0: a bad one, rows that see nothing).
-__device__ __forceinline__ long long tiles_of(int nq, long long len, int topk_tiles, int j) {
-  if (topk_tiles) return (long long)j * topk_tiles;
-  if (len < 0) return j;
-  const long long base = len - nq;                    // positions before the first query row
-  const long long none = min((long long)j, max(0ll, -base));  // rows that see nothing: one (empty) tile each
-  return none + tiles_below(max(0ll, base + j)) - tiles_below(max(0ll, base));
-}
 
 // Sixteen codes of each of a thread's four keys; zeros where the tile has no key at all.
 __device__ __forceinline__ void load_codes(uint4 (&w)[4], const uint8_t* const (&src)[4], int col, bool any) {
@@ -300,10 +284,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   pdl_wait();
 
   // ---------------------------------------------------------------- this CTA's share
-  // The rows stand behind each other on a line, each with the cost of its start and then its tiles; a CTA takes the tiles
-  // in its share of the line.  Against equal shares of tiles alone: 16 sequences of four drafted tokens 69 -> 62 us, 64 x
-  // 2048 selected rows 52.5 -> 49.6 us, 300 positions 16.6 -> 17.2 us (two sums to scan).  A cost of 1 or 3 tiles: 64 and
-  // 62 us, 52 and 51 us.
+  // (paged_share.cuh.)  Rows split with the cost of their start counted, against equal shares of tiles alone: 16 sequences
+  // of up to six drafted tokens 69 -> 62 us, 64 x 2048 selected rows 52.5 -> 49.6 us, 300 positions 16.6 -> 17.2 us (two
+  // sums to scan).  A cost of 1 or 3 tiles: 64 and 62 us, 52 and 51 us.
   {
     longlong2* sums = reinterpret_cast<longlong2*>(smem);  // the warps' sums, in the rope half's room
     int* longest_s = reinterpret_cast<int*>(sums + 32);
@@ -346,50 +329,35 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const long long all_rows = __shfl_sync(0xffffffffu, all.y, 31);
     const int wb = max(warp - 1, 0);
     const longlong2 before = make_longlong2(__shfl_sync(0xffffffffu, all.x, wb), __shfl_sync(0xffffffffu, all.y, wb));
-    const long long cost = all_tiles > gridDim.x ? kPgRowCost : 0;  // (at most one tile each: nothing to balance)
-    const long long share = (all_tiles + cost * all_rows + gridDim.x - 1) / gridDim.x;
-    // Whole rows only, a CTA taking those that begin in its share, where that makes the longest walk little longer: by one
-    // tile, and by up to four more as more CTAs would leave partial results.  (64 rows of 256, 512, 1024 keys: 22.5, 28.2,
-    // 35.6 us split, 17.1, 23.0, 34.3 us whole; a chunk of 400 rows of 2048: 131 and 120 us; one row of 300 keys stays
-    // split, 14.3 us against 17.6.)
-    const long long ctas = gridDim.x;
-    const bool whole_rows =
-        (longest + cost) * ((all_rows + ctas - 1) / ctas) <= share + 1 + 5 * min(all_tiles, ctas) / kPgMaxGrid;
-    if (threadIdx.x == 64) start_s[3] = int(min(share, 1ll << 30));  // (a row has less than 2^24 tiles)
+    const PagedShares sh = paged_shares(all_tiles, all_rows, longest, int(gridDim.x));
+    if (threadIdx.x == 64) start_s[3] = int(min(sh.share, 1ll << 30));  // (a row has less than 2^24 tiles)
     const long long x0 = incl.x - mine.x + (warp ? before.x : 0), y0 = incl.y - mine.y + (warp ? before.y : 0);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {  // where the share begins, and where it ends
-      const long long g = share * (blockIdx.x + e);
-      long long x = x0, at = x0 + cost * y0;
-      if (g < at || g >= at + mine.x + cost * mine.y) continue;
+      const long long g = sh.begin(int(blockIdx.x) + e);
+      long long x = x0, at = sh.line(x0, y0);
+      if (g < at || g >= at + sh.line(mine.x, mine.y)) continue;
       for (int b = b0;; ++b) {
         const long long n = per == 1 ? mine.x : tiles(b, q0, nq, len, false);  // (one sequence: its numbers are at hand)
-        if (g < at + n + cost * nq) {
-          int lo = 0, hi = nq;  // the last row that begins at or before g
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tiles_of(nq, len, topk_tiles, mid) + cost * mid <= g - at) lo = mid;
-            else hi = mid;
-          }
-          const long long first = tiles_of(nq, len, topk_tiles, lo);
-          const long long off = g - at - first - cost * lo;
-          const int tile = int(!whole_rows ? max(0ll, off - cost)
-                               : off == 0  ? 0
-                                           : tiles_of(nq, len, topk_tiles, lo + 1) - first);  // (the next row's begin)
+        if (g < at + sh.line(n, nq)) {
+          long long first;
+          int tile;
+          const int row = sh.cut(nq, len, topk_tiles, g - at, first, tile);
           if (e == 0) {
             start_s[0] = b;
-            start_s[1] = q0 + lo;
+            start_s[1] = q0 + row;
             start_s[2] = tile;
           }
           ends_s[e] = x + first + tile;  // tiles before g
           break;
         }
         x += n;
-        at += n + cost * nq;
+        at += sh.line(n, nq);
       }
     }
-    if (threadIdx.x == 0 && share * (blockIdx.x + 1) >= all_tiles + cost * all_rows) ends_s[1] = all_tiles;
-    if (threadIdx.x == 32 && share * blockIdx.x >= all_tiles + cost * all_rows) ends_s[0] = all_tiles;
+    const long long end = sh.line(all_tiles, all_rows);
+    if (threadIdx.x == 0 && sh.begin(int(blockIdx.x) + 1) >= end) ends_s[1] = all_tiles;
+    if (threadIdx.x == 32 && sh.begin(int(blockIdx.x)) >= end) ends_s[0] = all_tiles;
   }
   tc_fence_before();
   __syncthreads();
