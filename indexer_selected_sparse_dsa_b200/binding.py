@@ -288,6 +288,14 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _rows(t, name):
+    """Length of a tensor's first dimension; what has none is found here, everything else by _check_all."""
+    try:
+        return t.shape[0]
+    except (AttributeError, IndexError, TypeError):
+        raise TypeError(f"{name} must be a CUDA tensor of at least one dimension") from None
+
+
 def _paged_sizes(seq_len, page_table, kv8):
     """(batch, max_pages, n_pages, page_size); a wrong number of dimensions is found here, wrong sizes by _check_all."""
     try:
@@ -326,7 +334,7 @@ def dsa_cache_read(kv8, kv_scale, seq_len, page_table, kv_start, kv, stream=None
     """Unpack every sequence of the paged cache to flat bf16 rows kv[kv_start[b] + s]."""
     import torch
     batch, max_pages, n_pages, page_size = _paged_sizes(seq_len, page_table, kv8)
-    cache_rows = kv.shape[0]
+    cache_rows = _rows(kv, "kv")
     i32, dev = torch.int32, _device()
     k8, ks, sl, pt, start, flat = _check_all(
         dev, (kv8, torch.uint8, (n_pages, page_size, ROW8), "kv8"),
@@ -340,19 +348,20 @@ def dsa_cache_read(kv8, kv_scale, seq_len, page_table, kv_start, kv, stream=None
 def _paged_attn(name, q, cu_q, seq_len, page_table, idx, kv8, kv_scale, scale, o_lat, lse, ws, stream):
     import torch
     batch, max_pages, n_pages, page_size = _paged_sizes(seq_len, page_table, kv8)
-    i32, f32, bf16, dev, T = torch.int32, torch.float32, torch.bfloat16, _device(), q.shape[0]
+    i32, f32, bf16, dev = torch.int32, torch.float32, torch.bfloat16, _device()
+    T, ws_bytes = _rows(q, "q"), _rows(ws, "ws")
+    if idx is not None and getattr(idx, "ndim", None) != 2:
+        raise TypeError("idx must be a tensor of 2 dimensions")
     qp, cu, sl, pt, k8, ks, op, lp, wp = _check_all(
         dev, (q, bf16, (T, HEADS, ROW), "q"), (cu_q, i32, (batch + 1,), "cu_q"), (seq_len, i32, (batch,), "seq_len"),
         (page_table, i32, (batch, max_pages), "page_table"), (kv8, torch.uint8, (n_pages, page_size, ROW8), "kv8"),
         (kv_scale, f32, (n_pages, page_size), "kv_scale"), (o_lat, bf16, (T, HEADS, LATENT), "o_lat"),
-        (lse, f32, (T, HEADS), "lse"), (ws, torch.uint8, (ws.numel(),), "ws"))
+        (lse, f32, (T, HEADS), "lse"), (ws, torch.uint8, (ws_bytes,), "ws"))
     sel = ()
     if idx is not None:
-        if getattr(idx, "ndim", None) != 2:
-            raise TypeError("idx must be a tensor of 2 dimensions")
         sel = (*_check_all(dev, (idx, i32, (T, idx.shape[1]), "idx")), idx.shape[1])
     _check(getattr(lib(), name)(qp, T, cu, sl, pt, batch, max_pages, *sel, k8, ks, n_pages, page_size, scale, op, lp, wp,
-                                ws.numel(), _raw_stream(stream, dev)))
+                                ws_bytes, _raw_stream(stream, dev)))
 
 
 def dsa_paged_mla_attn(q, cu_q, seq_len, page_table, kv8, kv_scale, scale, o_lat, lse, ws, stream=None):

@@ -177,3 +177,29 @@ def test_a_short_limit_times_out_or_gives_the_result():
     r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\nLIMITS = {limits!r}\n" + SHORT], capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and "RESULT True True True" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ arguments that are no tensors (CPU)
+
+@pytest.mark.parametrize("bad", [None, 3, [1.0]], ids=str)
+def test_arguments_that_are_no_tensors(bad):
+    """As everywhere: a TypeError that names the argument, whichever it is."""
+    import torch
+    i32 = torch.zeros(3, dtype=torch.int32)
+    good = dict(q=torch.zeros(2, HEADS, ROW, dtype=torch.bfloat16), cu_q=i32, seq_len=i32[:2], page_table=i32[:2].view(2, 1),
+                idx=torch.zeros(2, 5, dtype=torch.int32), kv8=torch.zeros(4, 8, ROW8, dtype=torch.uint8),
+                kv_scale=torch.zeros(4, 8), o=torch.zeros(2, HEADS, LATENT, dtype=torch.bfloat16),
+                ws=torch.zeros(1 << 10, dtype=torch.uint8), rows=torch.zeros(2, ROW, dtype=torch.bfloat16),
+                start=torch.zeros(2, dtype=torch.int64), kv=torch.zeros(9, ROW, dtype=torch.bfloat16))
+    calls = dict(
+        q=lambda a: B.dsa_paged_mla_attn(a["q"], a["cu_q"], a["seq_len"], a["page_table"], a["kv8"], a["kv_scale"], SCALE,
+                                         a["o"], None, a["ws"]),
+        idx=lambda a: B.dsa_paged_sparse_mla_attn(a["q"], a["cu_q"], a["seq_len"], a["page_table"], a["idx"], a["kv8"],
+                                                  a["kv_scale"], SCALE, a["o"], None, a["ws"]),
+        rows=lambda a: B.dsa_cache_write(a["rows"], a["cu_q"], a["seq_len"], a["page_table"], a["kv8"], a["kv_scale"]),
+        kv=lambda a: B.dsa_cache_read(a["kv8"], a["kv_scale"], a["seq_len"], a["page_table"], a["start"], a["kv"]))
+    for which, names in (("q", ("q", "ws", "kv8")), ("idx", ("q", "ws", "idx", "page_table")), ("rows", ("rows", "seq_len")),
+                         ("kv", ("kv", "kv8"))):
+        for name in names:
+            with pytest.raises(TypeError, match=f"^{name} must be"):
+                calls[which]({**good, name: bad})
