@@ -198,7 +198,7 @@ def test_arguments_that_are_no_tensors(bad):
                                                   a["kv_scale"], SCALE, a["o"], None, a["ws"]),
         rows=lambda a: B.dsa_cache_write(a["rows"], a["cu_q"], a["seq_len"], a["page_table"], a["kv8"], a["kv_scale"]),
         kv=lambda a: B.dsa_cache_read(a["kv8"], a["kv_scale"], a["seq_len"], a["page_table"], a["start"], a["kv"]))
-    for which, names in (("q", ("q", "ws", "kv8")), ("idx", ("q", "ws", "idx", "page_table")), ("rows", ("rows", "seq_len")),
+    for which, names in (("q", ("q", "ws", "kv8")), ("idx", ("q", "ws", "idx", "page_table")), ("rows", ("seq_len", "page_table")),
                          ("kv", ("kv", "kv8"))):
         for name in names:
             with pytest.raises(TypeError, match=f"^{name} must be"):
