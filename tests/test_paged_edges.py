@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from indexer_selected_sparse_dsa_b200 import binding as B
-from paged_util import HEADS, LATENT, ROW, ROW8, SCALE, Batch, check_attention, quantise64
+from paged_util import HEADS, LATENT, ROW, ROW8, SCALE, Batch, check_attention, quantise64, selection
 from test_paged_cache import bad_status, run_dense, run_selected
 
 
@@ -177,6 +177,87 @@ def test_a_short_limit_times_out_or_gives_the_result():
     r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\nLIMITS = {limits!r}\n" + SHORT], capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and "RESULT True True True" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ other arguments
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0416, 0.1352, 1.7])
+def test_scales_that_are_no_power_of_two(scale):
+    import torch
+    c = Batch([1, 4, 40], [2500, 300, 700], 16, seed=44)
+    o, lse = c.outputs()
+    ws = B.workspace(B.DSA_OP_PAGED_MLA, c.T, c.table.shape[1] * c.page, 0)
+    B.dsa_paged_mla_attn(c.q, *c.plan, c.kv8, c.kv_scale, scale, o, lse, ws)
+    B.dsa_sync_status()
+    check_attention(c, o, lse, scale=scale)
+    idx = selection(c, 300, seed=45, holes=0.2)
+    B.dsa_paged_sparse_mla_attn(c.q, *c.plan, torch.from_numpy(idx).cuda(), c.kv8, c.kv_scale, scale, o, lse, ws)
+    B.dsa_sync_status()
+    check_attention(c, o, lse, idx, scale=scale)
+
+
+@pytest.mark.gpu
+def test_without_lse():
+    """The outputs are the same; whole rows and rows split over CTAs (the merge) alike."""
+    import torch
+    c = Batch([1, 1, 1] + [1] * 60, [6000, 129, 128] + [20] * 60, 16, seed=46)
+    idx = selection(c, 900, seed=47)
+    idx_d = torch.from_numpy(idx).cuda()
+    want, want_s = run_dense(c)[0], run_selected(c, idx)[0]
+    ws = B.workspace(B.DSA_OP_PAGED_MLA, c.T, c.table.shape[1] * c.page, 0)
+    o, o_s = c.outputs()[0], c.outputs()[0]
+    B.dsa_paged_mla_attn(c.q, *c.plan, c.kv8, c.kv_scale, SCALE, o, None, ws)
+    B.dsa_paged_sparse_mla_attn(c.q, *c.plan, idx_d, c.kv8, c.kv_scale, SCALE, o_s, None, ws)
+    B.dsa_sync_status()
+    assert torch.equal(o, want) and torch.equal(o_s, want_s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("topk", [64, 2048])
+def test_what_the_indexer_selects_is_what_is_attended_to(topk):
+    """The selected step of a server: new rows written, positions ranked by the indexer, attention over what it wrote, one
+    behind the other on a stream; then all of it captured and replayed with other queries and lengths."""
+    import torch
+    c = Batch([1, 3, 1, 20], [5000, 900, 1, 2600], 16, seed=48)
+    g = torch.Generator(device="cuda").manual_seed(49)
+    q_I = torch.randn(c.T, B.INDEX_HEADS, B.INDEX_DIM, generator=g, device="cuda").bfloat16()
+    w = torch.rand(c.T, B.INDEX_HEADS, generator=g, device="cuda").bfloat16()
+    k_I = torch.randn(sum(c.lens), B.INDEX_DIM, generator=g, device="cuda").bfloat16()
+    first = np.concatenate([[0], np.cumsum(c.lens)[:-1]])
+    kv_start = torch.from_numpy(np.repeat(first, c.new)).cuda()
+    n_vis = torch.tensor([m - n + j + 1 for n, m in zip(c.new, c.lens) for j in range(n)], dtype=torch.int32, device="cuda")
+    new = torch.randn(c.T, ROW, generator=g, device="cuda").bfloat16()
+    idx = torch.full((c.T, topk), 7, dtype=torch.int32, device="cuda")
+    o, lse = c.outputs()
+    ws_i = B.workspace(B.DSA_OP_INDEXER_TOPK, c.T, max(c.lens), topk)
+    ws = B.workspace(B.DSA_OP_PAGED_MLA, c.T, c.table.shape[1] * c.page, topk)
+
+    def step():
+        B.dsa_cache_write(new, *c.plan, c.kv8, c.kv_scale)
+        B.dsa_indexer_topk(q_I, w, k_I, kv_start, n_vis, max(c.lens), topk, idx, ws_i)
+        B.dsa_paged_sparse_mla_attn(c.q, *c.plan, idx, c.kv8, c.kv_scale, SCALE, o, lse, ws)
+
+    def look():
+        B.dsa_sync_status()
+        kept = torch.minimum(n_vis, torch.tensor(topk, device="cuda"))
+        assert torch.equal((idx >= 0).sum(1, dtype=torch.int32), kept) and bool((idx < n_vis[:, None]).all())
+        check_attention(c, o, lse, idx.cpu().numpy())
+
+    step()
+    look()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([4000, 700, 1, 2000], [130, 3, 1, 20]):
+        q_I.normal_(generator=g)
+        c.q.normal_(generator=g)
+        new.normal_(generator=g)
+        c.lens = lens
+        c.seq_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        n_vis.copy_(torch.tensor([m - n + j + 1 for n, m in zip(c.new, lens) for j in range(n)], dtype=torch.int32))
+        graph.replay()
+        look()
 
 
 # ------------------------------------------------------------------ arguments that are no tensors (CPU)
