@@ -146,7 +146,6 @@ struct TileWalk {
     left = tiles;
     row_end = cu_q[b + 1];
     enter_row();
-    if (tile == ntiles) advance(0);
   }
   // the tiles of this CTA in the current row
   __device__ __forceinline__ int segment() const { return min(ntiles - tile, left); }

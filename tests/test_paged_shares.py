@@ -80,8 +80,6 @@ def walks(rows, begin_row, begin_tile, cost):
         if (r0, t0) == (r1, t1):
             out.append(0)
             continue
-        if t0 == (rows[r0] if r0 < len(rows) else 0):
-            r0, t0 = r0 + 1, 0
         n = sum(rows[r0:r1]) - t0 + t1
         starts = (r1 - r0) + (1 if t1 > 0 else 0) - (1 if t0 > 0 else 0)
         out.append(n + cost * starts)
@@ -95,7 +93,7 @@ def check(L, new, lens, topk_tiles=0, ctas=148):
     before = np.concatenate([[0], np.cumsum(rows)])
     assert tiles_at[0] == 0 and tiles_at[-1] == total and (np.diff(tiles_at) >= 0).all()
     for t, r, i in zip(tiles_at, rows_at, tile_at):  # the row and tile are the place that the count of tiles says
-        assert t == before[r] + i and 0 <= i <= (rows[r] if r < len(rows) else 0)
+        assert t == before[r] + i and 0 <= i < (rows[r] if r < len(rows) else 1)
     cost = 2 if total > ctas else 0
     assert share == -(-(total + cost * len(rows)) // ctas)
     most = max(walks(rows, rows_at, tile_at, cost))
