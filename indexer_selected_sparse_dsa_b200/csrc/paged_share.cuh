@@ -45,13 +45,14 @@ struct PagedShares {
   int cost;         // of a row's start, in tiles
   long long share;  // split: length of a CTA's part of the line
   int ctas;
-  int rows_each, rows_rest;  // whole: rows of each CTA, and rows / CTAs' remainder
+  long long rows_each;  // whole: rows of each CTA ...
+  int rows_rest;        // ... and the remainder (64 bits: a cu_q out of order may count rows many times)
 
   // Length of rows with that many tiles on the line.
   DSA_HD long long line(long long tiles, long long rows) const { return whole ? rows : tiles + cost * rows; }
   // Where a CTA's part begins, and (of the next one) ends.
   DSA_HD long long begin(int cta) const {
-    return whole ? (long long)cta * rows_each + unsigned(cta * rows_rest) / unsigned(ctas) : share * cta;
+    return whole ? cta * rows_each + unsigned(cta * rows_rest) / unsigned(ctas) : share * cta;
   }
   // The row of a sequence, and its tile, that point `off` of the sequence's part of the line lies in; and the tiles of
   // the rows before it.
@@ -75,9 +76,9 @@ DSA_HD PagedShares paged_shares(long long tiles, long long rows, int longest, in
   s.cost = tiles > ctas ? kPgRowCost : 0;  // (at most one tile each: nothing to balance)
   s.share = (tiles + s.cost * rows + ctas - 1) / ctas;
   s.ctas = ctas;
-  s.rows_each = int(rows / ctas);
+  s.rows_each = rows / ctas;
   s.rows_rest = int(rows % ctas);
-  const long long walk = (long long)(longest + s.cost) * (s.rows_each + (s.rows_rest ? 1 : 0));
+  const long long walk = (longest + s.cost) * (s.rows_each + (s.rows_rest ? 1 : 0));
   // One tile more, and up to four as more CTAs would leave partial results.
   s.whole = walk <= s.share + 1 + 5 * (tiles < ctas ? tiles : ctas) / kPgMaxGrid;
   return s;

@@ -134,6 +134,19 @@ def test_rows_near_the_number_of_ctas_are_dealt_out_one_by_one(lib):
         assert whole and most <= 66
 
 
+def test_rows_counted_many_times_over(lib):
+    """A cu_q that goes back and forth: more rows than 32 bits hold, and every place on the line still found."""
+    batch, rows = 12000, 1 << 25
+    for topk_tiles, m in ((1, 1 << 26), (16, 1 << 26), (0, rows)):
+        whole, tiles_at, rows_at, tile_at, _ = cuts(lib, [rows] * batch, [m] * batch, topk_tiles, 148)
+        each = lib.row_tiles(rows, m, topk_tiles, rows)
+        assert tiles_at[0] == rows_at[0] == 0 and tiles_at[-1] == batch * each and rows_at[-1] == batch * rows
+        assert (np.diff(tiles_at) > 0).all()
+        for t, r, i in zip(tiles_at, rows_at, tile_at):
+            b, j = divmod(int(r), rows)
+            assert int(t) == b * each + lib.row_tiles(rows, m, topk_tiles, j) + int(i)
+
+
 def test_tiles_of_by_definition(lib):
     for nq, m in ((1, 1), (5, 5), (7, 3), (4, 0), (300, 1000), (130, 129), (2, 1 << 20)):
         for j in range(0, nq + 1, max(1, nq // 9)):
