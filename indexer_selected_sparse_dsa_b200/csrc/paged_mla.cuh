@@ -137,7 +137,7 @@ struct TileWalk {
     const int len = seq_len[b];
     const long long n = (len > max_positions(c)) ? 0 : (long long)len - (row_end - t) + 1;
     seen = n < 1 ? 0 : int(n);
-    ntiles = topk_tiles ? topk_tiles : max(1, (seen + 127) >> 7);
+    ntiles = topk_tiles ? topk_tiles : max(1, int((unsigned(seen) + 127u) >> 7));
   }
   __device__ __forceinline__ void start(const int* at, int tiles) {
     b = at[0];

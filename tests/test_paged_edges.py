@@ -260,6 +260,27 @@ def test_what_the_indexer_selects_is_what_is_attended_to(topk):
         look()
 
 
+# ------------------------------------------------------------------ the longest sequence
+
+@pytest.mark.gpu
+def test_a_sequence_as_long_as_the_type_allows():
+    """2^31 - 64 positions, all of them the same page: o is the page's own, lse is log(number of pages) more.  A thread adds
+    2^31 / 128 / 148 * 16 weights of a head and 32 keys one by one in fp32, so its sum may be off by 2^-24 of it each,
+    0.108 in all (0.115 in lse); the value product's, in half as many steps of up to 2^-23, by as much."""
+    import torch
+    c = Batch([1], [64], 64, seed=50)
+    ro, rl, _, _ = c.reference()
+    pages = (1 << 25) - 1
+    table = torch.full((1, pages), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    length = torch.tensor([64 * pages], dtype=torch.int32, device="cuda")
+    o, lse = c.outputs()
+    ws = B.workspace(B.DSA_OP_PAGED_MLA, 1, 64 * pages, 0)
+    B.dsa_paged_mla_attn(c.q, c.cu_q, length, table, c.kv8, c.kv_scale, SCALE, o, lse, ws)
+    B.dsa_sync_status()
+    assert float((lse.double() - (rl + math.log(pages))).abs().max()) <= 0.115 + 2.0 ** -8
+    assert float((o.double() - ro).norm() / ro.norm()) <= 0.25 + 2.0 ** -8
+
+
 # ------------------------------------------------------------------ arguments that are no tensors (CPU)
 
 @pytest.mark.parametrize("bad", [None, 3, [1.0]], ids=str)
