@@ -59,6 +59,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "paged_cache.cuh"
 #include "paged_share.cuh"
@@ -1107,7 +1109,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_mla_merge_kernel(const in
 
 // Room for every CTA's two partial results, behind the CTAs' split rows.
 inline int paged_mla_grid(int T, int64_t max_keys, int sm_count) {
-  const int64_t tiles = int64_t(T) * ((max_keys + 127) / 128);
+  const int64_t tiles = int64_t(T) * ((std::min<int64_t>(max_keys, INT32_MAX) + 127) / 128);  // (a length is an int32)
   const int64_t most = sm_count < kPgMaxGrid ? sm_count : kPgMaxGrid;
   return int(tiles < most ? tiles : most);
 }

@@ -262,6 +262,14 @@ def test_what_the_indexer_selects_is_what_is_attended_to(topk):
 
 # ------------------------------------------------------------------ the longest sequence
 
+def test_workspace_of_any_length():
+    """Lengths end at 2^31 - 1, whatever max_pages * page_size says: the size does not shrink again."""
+    most = B.dsa_workspace_size(B.DSA_OP_PAGED_MLA, 1 << 20, 1 << 30, 0)
+    for T, keys in ((1 << 24, 1 << 60), (1 << 11, (1 << 62) - 1), (1 << 20, 1 << 50)):
+        assert B.dsa_workspace_size(B.DSA_OP_PAGED_MLA, T, keys, 0) == most
+    assert B.dsa_workspace_size(B.DSA_OP_PAGED_MLA, 1, (1 << 63) - 1, 0) == most
+
+
 @pytest.mark.gpu
 def test_a_sequence_as_long_as_the_type_allows():
     """2^31 - 64 positions, all of them the same page: o is the page's own, lse is log(number of pages) more.  A thread adds
