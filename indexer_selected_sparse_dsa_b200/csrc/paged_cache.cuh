@@ -82,9 +82,10 @@ __device__ __forceinline__ int row_exponent(uint32_t bits) {
 
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float(uint32_t(k + 127) << 23); }
 
-// What has to move is 1152 bytes in and 644 out a row, and that is what bounds it: 32768 rows take 13.4 us (4.4 TB/s,
-// 0.78 of the 10.4 us at the measured copy rate), 8 rows 2.0 us, a launch.  One warp per row, so that the row's largest
-// value is one warp reduction; four rows a warp, for more loads in flight, took 15.8 us.  Lane l holds latent
+// What has to move is 1152 bytes in and 644 out a row: 37913 rows take 15.7 us from HBM (4.3 TB/s, 0.66 of the measured
+// copy rate, at which they would take 10.4 us), 13.6 us again and again where they stay in L2; 13 rows 2.0 us, a launch.
+// One warp per row, so that the row's largest value is one warp reduction; four rows a warp, for more loads in flight, took
+// 15.8 us where one took 13.9, from L2 (from HBM it was not tried).  Lane l holds latent
 // values 8 l .. 8 l + 7, 256 + 8 l .. + 7 and rope values 2 l, 2 l + 1, so every load and store is whole lines.
 __global__ void __launch_bounds__(kCacheThreads)
     cache_write_kernel(const uint16_t* __restrict__ rows, long long rows_ld, int T, const int32_t* __restrict__ cu_q,
@@ -162,11 +163,11 @@ __device__ __forceinline__ int read_len(const PagedCache& c, const int32_t* seq_
 
 // The rows of all sequences, in order, are cut into equal shares, one per CTA.
 // Each CTA finds the sequence its share starts in with one scan over the
-// lengths; from there its warps walk on, one row per warp at a time.  Bounded by
-// the 1796 bytes a row that move: 65K rows of 16 ragged sequences take 20.0 us
-// (0.89 of 17.8 us at the measured copy rate); one sequence of 777 rows 4.2 us,
-// of which the chain length, table, page, row is most (four rows at a time
-// per warp made that 5.4 us).
+// lengths; from there its warps walk on, one row per warp at a time.  1796 bytes
+// a row have to move: 64850 rows of 16 ragged sequences take 24.4 us from HBM (0.73
+// of the measured copy rate, at which they would take 17.8 us), 20.2 us with part of
+// them in L2; one sequence of 777 rows 4.2 us, of which the chain length, table,
+// page, row is most (four rows at a time per warp made that 5.4 us).
 __global__ void __launch_bounds__(kCacheThreads)
     cache_read_kernel(PagedCache c, const int32_t* __restrict__ seq_len, const int64_t* __restrict__ kv_start,
                       uint16_t* __restrict__ kv, long long cache_rows) {

@@ -7,7 +7,9 @@
 //
 // Scores straight from the codes.  The query of a head is split once into
 // q = 2^e (hi + lo / 16), both e4m3 (4 + 4 significant bits: exact for values
-// within 2^5 of the head's largest, never off by more than 2^-22 of it), so
+// within 2^13 of the head's largest, as lo's smallest step, 2^-9, is 2^-13 of 1 in
+// hi's units, where that value is 224 to 448; below, off by half of it, 2^-21.8 of
+// the largest at most), so
 // the 8-bit tensor path multiplies the cache's codes as they lie in memory:
 // M = 128 rows, 64 of hi and 64 of lo.  The rope half follows in bf16 on top: half
 // of the query on the hi rows and eight times it on the lo rows, both exact.  (Zero
@@ -32,19 +34,21 @@
 // of the same keys: maximum, sum and scale of a head are registers, not a reduction
 // over threads.
 //
-// What bounds it: per 128-key tile the tensor pipe works 1024 (codes) + 260 (rope)
-// + 1600 (values; M = 128, N = 64 takes 50 cycles a step, the operands' reads from
-// shared memory) = 2900 cycles, and shared memory moves 80 KB of codes in and 96 KB
-// of operands out for S, 128 KB of widened values in and 192 KB out for O, 16 KB of
-// P: some 4300 cycles at 128 bytes each, against 3500 that a tile's 82 KB take from
-// HBM.  Measured 5400 cycles a tile, 11000 more where a CTA goes on to another query
-// row.  64 sequences of 2K to 16K positions, one token: 130 us (3.2 TB/s, 0.50 of
-// the measured copy rate); 512 tokens over 8192 positions: 0.81 ms (800 TFLOP/s,
-// 0.50 of the measured bf16 rate); 64 x 2048 selected rows: 49 us.
+// What bounds it: per 128-key tile the tensor pipe is busy for 2300 cycles by its
+// counter (2900 by the steps' measured times: 1024 codes, 260 rope, 1600 values at
+// M = 128, N = 64), and shared memory moves 80 KB of codes in and 96 KB of operands
+// out for S, 128 KB of widened values in and 192 KB out for O, 16 KB of P and 32 KB
+// of the softmax's tables: 544 KB, 4350 cycles at 128 bytes each, against 3500 that a
+// tile's 82 KB take from HBM.  Measured 5500 cycles a tile (a chunk of 148 rows,
+// start and results included).  64 sequences of 2K to 16K positions, one token: 130
+// us (3.3 TB/s, 0.50 of the measured copy rate; 147-157 us in a long run, with the
+// clock at 1.6 GHz under the power cap); 778 tokens of two prompts' chunks, 512 of
+// them over 8192 positions: 0.77-0.85 ms (760 to 840 TFLOP/s, 0.47 to 0.52 of the
+// measured bf16 rate); 64 x 2048 selected rows: 49 us.
 //
-// One CTA walks an equal share of all 128-key tiles of the batch (a change of the
-// query row counts as two more), query row after query row; a row that ends in another CTA leaves partial sums that
-// paged_mla_merge_kernel joins.  20 warps:
+// The batch's 128-key tiles are shared out over the CTAs (paged_share.cuh), a CTA
+// walking query row after query row; a row that ends in another CTA leaves partial
+// sums that paged_mla_merge_kernel joins.  20 warps:
 //  * warp 3 finds each key's cache row and 2^k, up to four tiles ahead;
 //  * warps 0 and 1 copy the tile's rows with cp.async, four chunks of 128 codes and
 //    the rope chunk, each 128 bytes of 128 keys;
