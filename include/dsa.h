@@ -404,7 +404,9 @@ DSA_API int dsa_sync_status(dsa_stream_t stream);
  * operation it started finish, releases its resources and exits, and the
  * timeout bit reported by dsa_sync_status as DSA_ERR_TIMEOUT is raised; the
  * outputs of that call are then undefined, the CUDA context stays usable.
- * (A waiting warp reads the clock every few microseconds.)  0 restores the
+ * (A waiting warp looks at the time every few microseconds; the paged attention
+ * counts the SM's cycles, two a nanosecond, so its waits are never shorter than
+ * the limit, and longer by as much as the clock is below 2 GHz.)  0 restores the
  * default (environment variable DSA_WAIT_LIMIT_NS, else 1.5 s).  Takes effect
  * for launches after the call; process-wide.
  */
